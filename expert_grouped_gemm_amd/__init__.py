@@ -20,7 +20,8 @@ __all__ = [
     "MoEError", "Problem", "WorkspaceLayout", "lib", "make_problem", "workspace_size", "workspace_layout",
     "workspace_views", "route_topk", "dispatch", "dispatch_noalloc", "expert_forward", "combine", "layer_forward",
     "check_workspace", "tile_trace", "schedule_of", "store_burst_probe", "owner_plan", "owner_gather",
-    "segment_copy", "expert_forward_signal", "segment_copy_wait", "SCHED", "DTYPE", "STATUS",
+    "segment_copy", "expert_forward_signal", "segment_copy_wait", "combine_backward", "dispatch_backward",
+    "mxfp4_quantize", "mxfp4_dequantize", "SCHED", "DTYPE", "STATUS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -114,6 +115,14 @@ def lib() -> ctypes.CDLL:
         L.moe_segment_copy_wait.restype = ctypes.c_int
         L.moe_segment_copy_wait.argtypes = [PP, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P,
                                             ctypes.c_int64, _P, ctypes.c_int, _P]
+        L.moe_combine_backward.restype = ctypes.c_int
+        L.moe_combine_backward.argtypes = [PP] + [_P] * 9
+        L.moe_dispatch_backward.restype = ctypes.c_int
+        L.moe_dispatch_backward.argtypes = [PP] + [_P] * 5
+        L.moe_mxfp4_quantize.restype = ctypes.c_int
+        L.moe_mxfp4_quantize.argtypes = [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]
+        L.moe_mxfp4_dequantize.restype = ctypes.c_int
+        L.moe_mxfp4_dequantize.argtypes = [_P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P]
         L.moe_schedule_of.restype = ctypes.c_int
         L.moe_schedule_of.argtypes = [PP]
         L.moe_tile_clock_hz.restype = ctypes.c_double
@@ -176,6 +185,47 @@ def _stream(stream) -> int:
 def _check(status: int, where: str):
     if status != 0:
         raise MoEError(status, where)
+
+
+def _operand(where: str, name: str, t, dtype, numel: int, optional: bool = False) -> Optional[int]:
+    """The address of a call's tensor, once its type and size are the ones the
+    library will assume (the C ABI sees only a pointer)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{where}: {name} is missing")
+    ptr = _ptr(t)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{where}: {name} holds {t.numel()} elements, needs {numel}")
+    return ptr
+
+
+class _On:
+    """The device of a call's tensors made current, for the launch (a kernel
+    runs on the device that is current): every tensor has to be on it, and a
+    given stream has to be one of its streams."""
+
+    def __init__(self, where: str, stream, *tensors):
+        devs = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.device.type == "cuda"}
+        if len(devs) > 1:
+            raise ValueError(f"{where}: tensors on several devices {sorted(map(str, devs))}")
+        self.dev = next(iter(devs), None)
+        if self.dev is not None and getattr(stream, "device", self.dev) != self.dev:
+            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {self.dev}")
+        self.stream = stream
+        self.guard = None
+
+    def __enter__(self) -> int:
+        if self.dev is not None and self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def workspace_size(p: Problem) -> int:
@@ -327,6 +377,70 @@ def layer_forward(p: Problem, X, X_scale, logits, W1, W1_scale, W2, W2_scale, Y,
                                    _ptr(W2), _ptr(W2_scale), _ptr(Y), _ptr(Y_fp32), _ptr(workspace),
                                    workspace.numel(), _ptr(topk_idx), _ptr(topk_w), _ptr(counts), _ptr(offsets),
                                    _ptr(row_src), _stream(stream)), "moe_layer_forward")
+
+
+def combine_backward(p: Problem, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf, d_topk_w, d_logits=None,
+                     stream=None):
+    """moe_combine_backward: the gradients of the combine's inputs (the expert
+    outputs in token-order slots, the gate weights) and, if d_logits is given,
+    of the router's logits."""
+    w, cap = "combine_backward", row_capacity(p)
+    buf_dt = torch.bfloat16 if p.flags & FLAG_BF16_COMBINE_BUF else torch.float32
+    args = (_operand(w, "dY", dY, torch.bfloat16, p.T * p.d),
+            _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d),
+            _operand(w, "tok_off", tok_off, torch.int32, p.T + 1),
+            _operand(w, "topk_idx", topk_idx, torch.int32, p.T * p.k),
+            _operand(w, "topk_w", topk_w, torch.float32, p.T * p.k),
+            _operand(w, "d_combine_buf", d_combine_buf, torch.bfloat16, cap * p.d),
+            _operand(w, "d_topk_w", d_topk_w, torch.float32, p.T * p.k),
+            _operand(w, "d_logits", d_logits, torch.float32, p.T * p.E_global, optional=True))
+    with _On(w, stream, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf, d_topk_w, d_logits) as s:
+        _check(lib().moe_combine_backward(ctypes.byref(p), *args, s), "moe_combine_backward")
+
+
+def dispatch_backward(p: Problem, d_x_slots, tok_off, dX, dX_fp32=None, stream=None):
+    """moe_dispatch_backward: dX[t] = the sum of the token's slots of d_x_slots."""
+    w = "dispatch_backward"
+    args = (_operand(w, "d_x_slots", d_x_slots, torch.bfloat16, row_capacity(p) * p.d),
+            _operand(w, "tok_off", tok_off, torch.int32, p.T + 1),
+            _operand(w, "dX", dX, torch.bfloat16, p.T * p.d),
+            _operand(w, "dX_fp32", dX_fp32, torch.float32, p.T * p.d, optional=True))
+    with _On(w, stream, d_x_slots, tok_off, dX, dX_fp32) as s:
+        _check(lib().moe_dispatch_backward(ctypes.byref(p), *args, s), "moe_dispatch_backward")
+
+
+def _mxfp4_shape(where: str, x):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError(f"{where}: expected a tensor of rows")
+    cols = x.shape[-1]
+    if cols < 1 or cols % 32:
+        raise ValueError(f"{where}: rows of {cols} elements are not whole blocks of 32")
+    return x.numel() // cols, cols
+
+
+def mxfp4_quantize(x, codes, scales, stream=None):
+    """moe_mxfp4_quantize: x [..., cols] (bf16 or fp32) into MXFP4, codes uint8
+    [..., cols/2] and E8M0 scales uint8 [..., cols/32], blocks along the last
+    dimension."""
+    w = "mxfp4_quantize"
+    rows, cols = _mxfp4_shape(w, x)
+    n = rows * cols
+    args = (_operand(w, "x", x, (torch.bfloat16, torch.float32), n), int(x.dtype == torch.float32), rows, cols,
+            _operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32))
+    with _On(w, stream, x, codes, scales) as s:
+        _check(lib().moe_mxfp4_quantize(*args, s), "moe_mxfp4_quantize")
+
+
+def mxfp4_dequantize(codes, scales, out, stream=None):
+    """moe_mxfp4_dequantize: the values of MXFP4 codes and scales into out
+    [..., cols] (bf16 or fp32)."""
+    w = "mxfp4_dequantize"
+    rows, cols = _mxfp4_shape(w, out)
+    n = rows * cols
+    args = (_operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32),
+            rows, cols, _operand(w, "out", out, (torch.bfloat16, torch.float32), n), int(out.dtype == torch.float32))
+    with _On(w, stream, codes, scales, out) as s:
+        _check(lib().moe_mxfp4_dequantize(*args, s), "moe_mxfp4_dequantize")
 
 
 def check_workspace(p: Problem, workspace, stream=None):

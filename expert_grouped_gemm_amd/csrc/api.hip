@@ -58,6 +58,14 @@ moe_status_t check_ws(const moe::Layout& L, const void* ws, size_t bytes) {
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
 
+// Shapes of the MXFP4 codec: whole blocks, and an element count that 64-bit
+// byte offsets hold with room to spare.
+moe_status_t check_mxfp4_shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (cols % 32 || cols > (1ll << 40) || (rows > 0 && cols > (1ll << 46) / rows)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // Whether a copier wavefront fits on a SIMD beside the expert GEMM's
 // wavefronts (two per SIMD): their register counts, as the runtime reports
 // them, rounded up to the allocation granule of 8, within the 512 registers
@@ -364,6 +372,51 @@ MOE_API moe_status_t moe_segment_copy_wait(const moe_problem_t* p, const float* 
   if (!copier_fits_beside_gemm(p->dtype)) return MOE_ERR_UNSUPPORTED;
   hipError_t e = moe::launch_segment_copy_wait(*p, O_pad, (int)R, segments, (int)n_segments, recv, (int)R_recv,
                                                row_done, err, grid ? grid : 256, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY, const void* combine_buf,
+                                          const int32_t* tok_off, const int32_t* topk_idx, const float* topk_w,
+                                          void* d_combine_buf, float* d_topk_w, float* d_logits, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!dY || !combine_buf || !tok_off || !topk_idx || !topk_w || !d_combine_buf || !d_topk_w)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(dY) || !aligned16(combine_buf) || !aligned16(d_combine_buf)) return MOE_ERR_INVALID_ARGUMENT;
+  if (combine_buf == d_combine_buf) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_combine_backward(*p, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf,
+                                                    d_topk_w, d_logits, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d_x_slots, const int32_t* tok_off,
+                                           void* dX, float* dX_fp32, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!d_x_slots || !tok_off || !dX || d_x_slots == dX) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(d_x_slots) || !aligned16(dX) || (dX_fp32 && !aligned16(dX_fp32))) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_dispatch_backward(*p, d_x_slots, tok_off, dX, dX_fp32, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, uint8_t* codes,
+                                        uint8_t* scales, void* stream) {
+  moe_status_t st = check_mxfp4_shape(rows, cols);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_mxfp4_quantize(x, x_fp32 != 0, rows * cols, codes, scales, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                          void* out, int out_fp32, void* stream) {
+  moe_status_t st = check_mxfp4_shape(rows, cols);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_mxfp4_dequantize(codes, scales, rows * cols, out, out_fp32 != 0,
+                                                    (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
 

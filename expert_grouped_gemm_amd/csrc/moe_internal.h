@@ -175,6 +175,19 @@ hipError_t launch_expert_forward_fused(const moe_problem_t& p, const Layout& L, 
                                        const void* W1, const void* W1_scale, const void* W2, const void* W2_scale,
                                        void* combine_buf, hipStream_t s);
 
+// Gradients of the combine (with the router's softmax) and of the dispatch
+// (validated arguments; see moe_combine_backward and moe_dispatch_backward).
+hipError_t launch_combine_backward(const moe_problem_t& p, const void* dY, const void* combine_buf,
+                                   const int32_t* tok_off, const int32_t* topk_idx, const float* topk_w, void* dO,
+                                   float* d_w, float* d_logits, hipStream_t s);
+hipError_t launch_dispatch_backward(const moe_problem_t& p, const void* d_x_slots, const int32_t* tok_off, void* dX,
+                                    float* dX_fp32, hipStream_t s);
+
+// MXFP4 codec over n elements (n % 32 == 0; validated arguments).
+hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t n, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out, bool f32,
+                                   hipStream_t s);
+
 // Owner-aligned return path (validated arguments; see moe_owner_plan,
 // moe_owner_gather and moe_segment_copy).
 struct OwnerPlanSizes {

@@ -414,6 +414,59 @@ MOE_API moe_status_t moe_segment_copy_wait(const moe_problem_t* p, const float* 
                                            int64_t R_recv, const int32_t* row_done, int64_t row_done_len,
                                            int32_t* err, int grid, void* stream);
 
+/* Gradients of the layer's two permutations, for a training step. Both work
+ * on any operand type of p (they touch none of the experts' operands).
+ *
+ * moe_combine_backward: the gradient of moe_combine with moe_route_topk's
+ * softmax behind it. dY bf16 [T, d] in output-row order q; combine_buf [cap,
+ * d] as moe_combine read it (fp32, or bf16 with MOE_FLAG_BF16_COMBINE_BUF);
+ * tok_off, topk_idx, topk_w of the forward call. Outputs:
+ *   d_combine_buf bf16 [cap, d]   slot p of token t, gate j: w[t,j] dY[q(t)],
+ *                                 rounded once; rows past the last slot untouched
+ *   d_topk_w fp32 [T, k]          <dY[q(t)], combine_buf[p]>, summed in fp32; 0
+ *                                 for an expert outside [e_begin, e_end)
+ *   d_logits fp32 [T, E_global]   or NULL: the gradient through the softmax over
+ *                                 the k selected logits, w_j (dw_j - sum_i w_i
+ *                                 dw_i), 0 for the others. It is linear in
+ *                                 d_topk_w: the shares' results add up to the
+ *                                 layer's gradient.
+ * A token whose slot range does not lie inside [0, cap) or does not hold as
+ * many slots as its topk_idx row has local experts gets NaN in d_topk_w and
+ * d_logits, and no slot of it is read or written. An expert id outside
+ * [0, E_global) has no column in d_logits.
+ *
+ * moe_dispatch_backward: the gradient of the dispatch's gather. d_x_slots bf16
+ * [cap, d] holds the gradient of every local row in token-order slots (as
+ * moe_expert_backward leaves it); dX bf16 [T, d], in token order, is the sum
+ * of the token's slots (ascending, in fp32, rounded once; 0 for a token
+ * without a local expert), dX_fp32 [T, d] (may be NULL) the same sums before
+ * the rounding. A token whose slot range does not lie inside [0, cap) gets
+ * NaN. */
+MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY, const void* combine_buf,
+                                          const int32_t* tok_off, const int32_t* topk_idx, const float* topk_w,
+                                          void* d_combine_buf, float* d_topk_w, float* d_logits, void* stream);
+MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d_x_slots, const int32_t* tok_off,
+                                           void* dX, float* dX_fp32, void* stream);
+
+/* MXFP4 codec (OCP MXFP4: E2M1 elements, two per byte, the even element in
+ * the low nibble; one E8M0 scale byte per 32 consecutive elements of a row).
+ * x [rows, cols], cols % 32 == 0, rows >= 0, DEVICE memory; codes uint8
+ * [rows, cols/2], scales uint8 [rows, cols/32]. codes 16-byte aligned.
+ *
+ * moe_mxfp4_quantize (x fp32 if x_fp32, else bf16): per block, scale =
+ * 2^(floor(log2 amax) - 2), at least 2^-127 (byte 0; byte 127 for a block of
+ * zeros), elements = x / scale rounded to nearest even, saturating at +-6. A
+ * block with an infinite or NaN element gets the scale byte 255 (NaN) and
+ * codes 0: every value read back from it, and every product with it, is NaN.
+ *
+ * moe_mxfp4_dequantize (out fp32 if out_fp32, else bf16): the values, exact
+ * (scale bytes above 252, which the quantiser does not write, may overflow to
+ * infinity). */
+MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, uint8_t* codes,
+                                        uint8_t* scales, void* stream);
+MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                          void* out, int out_fp32, void* stream);
+
 MOE_API const char* moe_status_string(moe_status_t s);
 MOE_API int moe_last_hip_error(void);
 /* Library version, e.g. "0.1.0". */

@@ -194,3 +194,29 @@ def test_binding_argument_counts_match_the_header(L):
         assert len(argtypes) == n, (name, len(argtypes), n)
         checked += 1
     assert checked >= 15
+
+
+def test_backward_and_codec_arguments_rejected_before_launch(L):
+    """The gradients of the permutations and the MXFP4 codec: NULL and misaligned pointers, aliased buffers, shapes."""
+    p = moe.make_problem(**GOOD)
+    P = ctypes.byref(p)
+    f, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 4)   # never dereferenced
+    g = ctypes.c_void_p(1 << 21)
+    good = [f, f, f, f, f, g, f, None, None]
+    for i in range(7):
+        assert L.moe_combine_backward(P, *[None if j == i else x for j, x in enumerate(good)]) == 1, i
+    for i in (0, 1, 5):
+        assert L.moe_combine_backward(P, *[odd if j == i else x for j, x in enumerate(good)]) == 1, i
+    assert L.moe_combine_backward(P, f, f, f, f, f, f, f, None, None) == 1
+    assert L.moe_combine_backward(None, *good) == 1
+    assert L.moe_dispatch_backward(P, None, f, g, None, None) == 1
+    assert L.moe_dispatch_backward(P, f, None, g, None, None) == 1
+    assert L.moe_dispatch_backward(P, f, f, f, None, None) == 1
+    assert L.moe_dispatch_backward(P, f, f, g, odd, None) == 1
+    for rows, cols, code in ((-1, 32, 1), (1, 0, 1), (1, 33, 2), (1 << 40, 1 << 20, 2)):
+        assert L.moe_mxfp4_quantize(f, 0, rows, cols, f, f, None) == code
+        assert L.moe_mxfp4_dequantize(f, f, rows, cols, f, 0, None) == code
+    assert L.moe_mxfp4_quantize(None, 0, 0, 32, None, None, None) == 0
+    assert L.moe_mxfp4_quantize(f, 0, 1, 32, odd, f, None) == 1
+    assert L.moe_mxfp4_quantize(f, 0, 1, 32, f, None, None) == 1
+    assert L.moe_mxfp4_dequantize(f, f, 1, 32, odd, 1, None) == 1
