@@ -21,7 +21,7 @@ __all__ = [
     "workspace_views", "route_topk", "dispatch", "dispatch_noalloc", "expert_forward", "combine", "layer_forward",
     "check_workspace", "tile_trace", "schedule_of", "store_burst_probe", "owner_plan", "owner_gather",
     "segment_copy", "expert_forward_signal", "segment_copy_wait", "combine_backward", "dispatch_backward",
-    "mxfp4_quantize", "mxfp4_dequantize", "SCHED", "DTYPE", "STATUS",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear1", "mxfp4_linear2", "SCHED", "DTYPE", "STATUS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -123,6 +123,9 @@ def lib() -> ctypes.CDLL:
         L.moe_mxfp4_quantize.argtypes = [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]
         L.moe_mxfp4_dequantize.restype = ctypes.c_int
         L.moe_mxfp4_dequantize.argtypes = [_P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P]
+        for name in ("moe_mxfp4_linear1", "moe_mxfp4_linear2"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [PP] + [_P] * 8 + [ctypes.c_size_t, _P]
         L.moe_schedule_of.restype = ctypes.c_int
         L.moe_schedule_of.argtypes = [PP]
         L.moe_tile_clock_hz.restype = ctypes.c_double
@@ -441,6 +444,34 @@ def mxfp4_dequantize(codes, scales, out, stream=None):
             rows, cols, _operand(w, "out", out, (torch.bfloat16, torch.float32), n), int(out.dtype == torch.float32))
     with _On(w, stream, codes, scales, out) as s:
         _check(lib().moe_mxfp4_dequantize(*args, s), "moe_mxfp4_dequantize")
+
+
+def mxfp4_linear1(p: Problem, X, X_scale, row_src, offsets, W1, W1_scale, H, workspace, stream=None):
+    """moe_mxfp4_linear1: the experts' first Linear with SwiGLU on MXFP4 tokens
+    (gathered through row_src, or already in expert order with row_src=None)
+    and MXFP4 weights, into H bf16 [cap, f]."""
+    w, u8, cap, El = "mxfp4_linear1", torch.uint8, row_capacity(p), p.e_end - p.e_begin
+    rows = cap if row_src is None else p.T
+    args = (_operand(w, "X", X, u8, rows * p.d // 2), _operand(w, "X_scale", X_scale, u8, rows * p.d // 32),
+            _operand(w, "row_src", row_src, torch.int32, cap, optional=True),
+            _operand(w, "offsets", offsets, torch.int32, El + 1),
+            _operand(w, "W1", W1, u8, El * p.f * p.d), _operand(w, "W1_scale", W1_scale, u8, El * p.f * p.d // 16),
+            _operand(w, "H", H, torch.bfloat16, cap * p.f), _operand(w, "workspace", workspace, u8, 0))
+    with _On(w, stream, X, X_scale, row_src, offsets, W1, W1_scale, H, workspace) as s:
+        _check(lib().moe_mxfp4_linear1(ctypes.byref(p), *args, workspace.numel(), s), "moe_mxfp4_linear1")
+
+
+def mxfp4_linear2(p: Problem, H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace, stream=None):
+    """moe_mxfp4_linear2: the experts' second Linear on MXFP4 rows and weights,
+    into the token-order slots of combine_buf."""
+    w, u8, cap, El = "mxfp4_linear2", torch.uint8, row_capacity(p), p.e_end - p.e_begin
+    buf_dt = torch.bfloat16 if p.flags & FLAG_BF16_COMBINE_BUF else torch.float32
+    args = (_operand(w, "H", H, u8, cap * p.f // 2), _operand(w, "H_scale", H_scale, u8, cap * p.f // 32),
+            _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
+            _operand(w, "W2", W2, u8, El * p.f * p.d // 2), _operand(w, "W2_scale", W2_scale, u8, El * p.f * p.d // 32),
+            _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d), _operand(w, "workspace", workspace, u8, 0))
+    with _On(w, stream, H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace) as s:
+        _check(lib().moe_mxfp4_linear2(ctypes.byref(p), *args, workspace.numel(), s), "moe_mxfp4_linear2")
 
 
 def check_workspace(p: Problem, workspace, stream=None):

@@ -399,6 +399,38 @@ MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
 
+MOE_API moe_status_t moe_mxfp4_linear1(const moe_problem_t* p, const uint8_t* X, const uint8_t* X_scale,
+                                       const int32_t* row_src, const int32_t* offsets, const uint8_t* W1,
+                                       const uint8_t* W1_scale, void* H, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!X || !X_scale || !offsets || !W1 || !W1_scale || !H) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(X) || !aligned16(X_scale) || !aligned16(W1) || !aligned16(W1_scale) || !aligned16(H))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const hipError_t e = moe::launch_mxfp4_linear(*p, L, static_cast<char*>(workspace), true, X, X_scale, row_src,
+                                                offsets, nullptr, W1, W1_scale, H, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_mxfp4_linear2(const moe_problem_t* p, const uint8_t* H, const uint8_t* H_scale,
+                                       const int32_t* offsets, const int32_t* row_dst, const uint8_t* W2,
+                                       const uint8_t* W2_scale, void* combine_buf, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (!H || !H_scale || !offsets || !row_dst || !W2 || !W2_scale || !combine_buf) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(H) || !aligned16(H_scale) || !aligned16(W2) || !aligned16(W2_scale) || !aligned16(combine_buf))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const hipError_t e = moe::launch_mxfp4_linear(*p, L, static_cast<char*>(workspace), false, H, H_scale, nullptr,
+                                                offsets, row_dst, W2, W2_scale, combine_buf, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
 MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, uint8_t* codes,
                                         uint8_t* scales, void* stream) {
   moe_status_t st = check_mxfp4_shape(rows, cols);

@@ -19,7 +19,46 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
             band_row0, band_rows, l2_full, wave_band0, meta);
 }
 
+// The plan for calls whose row indices come from the caller: row_src entries
+// outside [0, src_end) or row_dst entries outside [0, cap), among the rows the
+// offsets cover, empty the plan like bad offsets do (no tile runs, nothing is
+// read through them) and set their error bits. Either array may be null. One
+// block reads them all: 131072 rows are 128 coalesced loads per thread.
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap, int N1,
+                                                         int G, int Pmax, const int32_t* __restrict__ row_src,
+                                                         int64_t src_end, const int32_t* __restrict__ row_dst,
+                                                         int32_t* __restrict__ band_expert,
+                                                         int32_t* __restrict__ band_row0,
+                                                         int32_t* __restrict__ band_rows,
+                                                         int32_t* __restrict__ l2_full,
+                                                         int32_t* __restrict__ wave_band0, int32_t* __restrict__ meta) {
+  plan_body(offsets, El, cap, N1, G, 0, 1, Pmax, ARG_ERR_ALL, nullptr, 0, band_expert, band_row0, band_rows, l2_full,
+            wave_band0, meta);
+  const int lo = max(0, offsets[0]), hi = min(cap, offsets[El]);
+  bool bad_src = false, bad_dst = false;
+#pragma unroll 4
+  for (int r = lo + (int)threadIdx.x; r < hi; r += 1024) {
+    if (row_src) bad_src |= row_src[r] < 0 || row_src[r] >= src_end;
+    if (row_dst) bad_dst |= (unsigned)row_dst[r] >= (unsigned)cap;
+  }
+  const int any_src = __syncthreads_or(bad_src), any_dst = __syncthreads_or(bad_dst);
+  if (threadIdx.x == 0 && (any_src || any_dst)) {
+    meta[META_P] = 0;
+    __hip_atomic_fetch_or(meta + META_ARG_ERR, (any_src ? ARG_ERR_ROW_SRC : 0) | (any_dst ? ARG_ERR_ROW_DST : 0),
+                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
 }  // namespace
+
+hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
+                            const int32_t* row_src, const int32_t* row_dst, hipStream_t s) {
+  auto I = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(1024), 0, s, offsets, L.E_l, L.cap, 1, 1, L.Pmax, row_src,
+                     (int64_t)p.T * p.k, row_dst, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.l2_full),
+                     I(L.wave_band0), I(L.pub.meta));
+  return hipGetLastError();
+}
 
 int gemm_grid(const moe_problem_t& p) {
   static thread_local int cached_dev = -1;
@@ -179,6 +218,27 @@ hipError_t launch_expert_forward(const moe_problem_t& p, const Layout& L, char* 
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_gemm_schedule(p, P, G, s);
+}
+
+// One Linear of the experts on MXFP4 rows and MXFP4 weights (see
+// moe_mxfp4_linear1 / moe_mxfp4_linear2), as a launch of the persistent GEMM.
+hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const uint8_t* A,
+                               const uint8_t* A_scale, const int32_t* row_src, const int32_t* offsets,
+                               const int32_t* row_dst, const uint8_t* W, const uint8_t* W_scale, void* out,
+                               hipStream_t s) {
+  const int G = gemm_grid(p);
+  if (G <= 0) return hipErrorInvalidDevice;
+  const hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, s);
+  if (e != hipSuccess) return e;
+  GemmParams P = gemm_params(p, L, ws, G, A, nullptr, row_dst, W, nullptr, W, nullptr, out, nullptr, 0);
+  P.Xe = P.He = A_scale;
+  P.W1e = P.W2e = W_scale;
+  P.H = first ? static_cast<uint8_t*>(out) : const_cast<uint8_t*>(A);
+  P.a_src = row_src;
+  P.a_k = p.k;
+  P.trace = nullptr;
+  P.mode = first ? MODE_SEP_L1 : MODE_SEP_L2;
+  return launch_gemm_w4a4(P, G, s);
 }
 
 // moe_layer_forward's expert GEMMs: the fused dispatch kernel has already

@@ -75,6 +75,8 @@ struct GemmParams {
   void* C;                // combine_buf [cap, d]: fp32, or bf16 with c_bf16
   // fp8 only: block scales and the fp32 SwiGLU output before quantisation
   const float* Xs;        // [d/128, cap]  scale of X_perm row r, K block c at c*cap + r
+  const uint8_t* Xe;      // MXFP4 activations: E8M0 scales of the Linear-1 rows, d/32 per row
+  const uint8_t* He;      // ... and of the Linear-2 rows, f/32 per row
   const float* W1s;       // [E_l, 2f/128, d/128] (e4m3 weights)
   const float* W2s;       // [E_l, d/128, f/128]
   const uint8_t* W1e;     // MXFP4 weights: E8M0 scales [E_l, 2f, d/32]
@@ -116,6 +118,7 @@ struct GemmParams {
 hipError_t launch_gemm_bf16(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_fp8(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_w4a8(const GemmParams& P, int G, hipStream_t s);
+hipError_t launch_gemm_w4a4(const GemmParams& P, int G, hipStream_t s);
 const void* gemm_kernel_bf16();
 
 namespace {
@@ -154,6 +157,10 @@ struct Tile {
   const uint8_t* Eg;      // scale row of the first weight row of the first half
   const uint8_t* Eu;      // ... of the second half
   size_t epitch;          // bytes between consecutive scale rows
+  // MXFP4 activations only
+  const uint8_t* Ae;      // E8M0 bytes of the rows of A, epitch bytes each
+  int khalf;              // the K slice of which only the first half exists (K % 256 == 128), or -1
+  uint32_t srow[2];       // byte offset from Ae of the row this lane's scale loads read
   // Linear-1 with gathered rows: band row r is row a_src[r] / a_k of A
   // (which then points at X); null: row row0 + r
   const int32_t* a_src;
@@ -169,12 +176,15 @@ struct Tile {
 // Operand types of the expert GEMM (the template parameter OT): bf16
 // activations and weights; e4m3 activations and e4m3 weights with fp32
 // 128x128 block scales; e4m3 activations and MXFP4 weights (E2M1 elements,
-// one E8M0 scale per 32 along K).
-enum OperandType { OT_BF16 = 0, OT_FP8 = 1, OT_W4A8 = 2 };
-__host__ __device__ constexpr bool mxfp4_weights(int OT) { return OT == OT_W4A8; }
+// one E8M0 scale per 32 along K); MXFP4 activations and MXFP4 weights.
+enum OperandType { OT_BF16 = 0, OT_FP8 = 1, OT_W4A8 = 2, OT_W4A4 = 3 };
+__host__ __device__ constexpr bool mxfp4_weights(int OT) { return OT == OT_W4A8; }  // against e4m3 activations
+__host__ __device__ constexpr bool e4m3_acts(int OT) { return OT == OT_FP8 || OT == OT_W4A8; }
+// Operand types whose tiles may issue their successor's first stages (see Chain).
+__host__ __device__ constexpr bool chains_tiles(int OT) { return OT == OT_BF16 || OT == OT_W4A4; }
 
 // K bytes per row per pipeline stage: 64 bf16 values, or for fp8 one 128-wide
-// scale block of e4m3 values. (64-byte bf16 stages, which double the ring
+// scale block of e4m3 values, or 256 MXFP4 values (both operands). (64-byte bf16 stages, which double the ring
 // depth of a wide tile, were measured no faster on the compute-bound shapes
 // and slower on the bandwidth-bound ones.)
 __host__ __device__ constexpr int stage_k_bytes(bool) { return 128; }
@@ -188,11 +198,16 @@ __host__ __device__ constexpr int stage_kb_bytes(int OT) { return mxfp4_weights(
 // holds MB*32 rows of the band plus the NNB*64 weight rows, one stage's K of
 // each; with fp8 activations also the 256 row scales of the stage's K block
 // (1 KiB), and either the block's two fp32 weight scales (padded to 16
-// bytes) or, for MXFP4 weights, one dword of four E8M0 scales per weight row.
+// bytes) or, for MXFP4 weights, one dword of four E8M0 scales per weight row;
+// with MXFP4 activations the stage's eight E8M0 scales of every band row and
+// weight row (8 bytes each).
 __host__ __device__ constexpr int stage_a_bytes(int MB, int OT) { return MB * 32 * stage_k_bytes(OT); }
 __host__ __device__ constexpr int stage_b_bytes(int NNB, int OT) { return NNB * 64 * stage_kb_bytes(OT); }
 __host__ __device__ constexpr int stage_scale_bytes(int NNB, int OT) {
-  return OT == OT_FP8 ? kBM * 4 + 16 : OT == OT_W4A8 ? kBM * 4 + NNB * 64 * 4 : 0;
+  return OT == OT_FP8    ? kBM * 4 + 16
+         : OT == OT_W4A8 ? kBM * 4 + NNB * 64 * 4
+         : OT == OT_W4A4 ? kBM * 8 + NNB * 64 * 8
+                         : 0;
 }
 __host__ __device__ constexpr int stage_bytes(int MB, int NNB, int OT) {
   return stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT) + stage_scale_bytes(NNB, OT);
@@ -242,7 +257,7 @@ __host__ __device__ constexpr int stage_b_rows_per_round(int OT) {
 }
 __host__ __device__ constexpr int stage_loads(int MB, int NNB, int OT) {
   return (MB * 32 + stage_a_rows_per_round(OT) - 1) / stage_a_rows_per_round(OT) +
-         NNB * 64 / stage_b_rows_per_round(OT) + (OT ? 2 : 0);
+         NNB * 64 / stage_b_rows_per_round(OT) + (OT == OT_W4A4 ? 2 + NNB / 2 : OT ? 2 : 0);
 }
 
 // Wavefront grid of a tile of width NNB: WM wavefront rows x WN wavefront
@@ -327,16 +342,35 @@ __device__ __forceinline__ void issue_load(const Tile& t, int kt, lds_t* st, int
     const bool part = REM && j == NAF;
     const int r0 = part ? NAF * ROUND + w * RPW : (j * NW + w) * RPI;
     const int r = r0 + sub;
-    const uint8_t* g = t.A + (t.arow[j] + (uint32_t)(kt * KB + ((slot ^ chunk_swizzle<KB>(r)) << 4)));
+    uint32_t chunk = slot ^ chunk_swizzle<KB>(r);
+    // the half slice's missing chunks re-read the ones before them (no MFMA takes them)
+    if constexpr (OT == OT_W4A4) chunk &= kt == t.khalf ? 3 : 7;
+    const uint8_t* g = t.A + (t.arow[j] + (uint32_t)(kt * KB + (chunk << 4)));
     if (!part || sub < RPW) __builtin_amdgcn_global_load_lds(g, st + r0 * KB, 16, 0, 0);
   } else if (j < NA + NBW) {
     const int sub = lane / CHB, slot = lane % CHB;
     const int r0 = ((j - NA) * NW + w) * RPIB;
     const int r = r0 + sub;
     const uint8_t* base = r0 < half ? t.Bg : t.Bu;
-    const uint8_t* g =
-        base + (uint32_t)((r & (half - 1)) * (uint32_t)t.ldb + kt * KBB + ((slot ^ chunk_swizzle<KBB>(r)) << 4));
+    uint32_t chunk = slot ^ chunk_swizzle<KBB>(r);
+    if constexpr (OT == OT_W4A4) chunk &= kt == t.khalf ? 3 : 7;
+    const uint8_t* g = base + (uint32_t)((r & (half - 1)) * (uint32_t)t.ldb + kt * KBB + (chunk << 4));
     __builtin_amdgcn_global_load_lds(g, st + stage_a_bytes(MB, OT) + r0 * KBB, 16, 0, NT ? kCpolNT : 0);
+  } else if constexpr (OT == OT_W4A4) {
+    // E8M0 scales, 8 bytes per row as two dwords in consecutive lanes: two
+    // instructions for the 256 band rows, then NNB / 2 for the weight rows
+    lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
+    const int js = j - NA - NBW;
+    const uint32_t dw = kt == t.khalf ? 0 : lane & 1;  // the half slice has one dword
+    if (js < 2) {
+      const uint8_t* g = t.Ae + (t.srow[js] + (uint32_t)(kt * 8 + dw * 4));
+      __builtin_amdgcn_global_load_lds(g, ss + (js * NW + w) * 256, 4, 0, 0);
+    } else {
+      const int r0 = ((js - 2) * NW + w) * 32, r = r0 + (lane >> 1);
+      const uint8_t* base = r0 < half ? t.Eg : t.Eu;
+      const uint8_t* g = base + (uint32_t)((r & (half - 1)) * (uint32_t)t.epitch + kt * 8 + dw * 4);
+      __builtin_amdgcn_global_load_lds(g, ss + kBM * 8 + r0 * 8, 4, 0, 0);
+    }
   } else if constexpr (OT != OT_BF16) {
     lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     if (j == NA + NBW) {
@@ -387,6 +421,14 @@ __device__ __forceinline__ void fill_arow(Tile& t, int tid) {
     // limits keep cap * d and cap * f (cap >= T) below 2^31 elements of at
     // most 2 bytes.
     t.arow[j] = (uint32_t)(t.a_src ? t.a_src[t.row0 + gr] / t.a_k : gr) * (uint32_t)t.lda;
+  }
+  if constexpr (OT == OT_W4A4) {
+#pragma unroll
+    for (int js = 0; js < 2; ++js) {
+      const int r = (js * NW + w) * 32 + ((tid & 63) >> 1);
+      const int gr = r < t.rows ? r : t.rows - 1;
+      t.srow[js] = (uint32_t)(t.a_src ? t.a_src[t.row0 + gr] / t.a_k : gr) * (uint32_t)t.epitch;
+    }
   }
 }
 
@@ -585,10 +627,67 @@ __device__ __forceinline__ void compute_stage_w4(const lds_t* sa, const lds_t* s
   }
 }
 
+// MXFP4 x MXFP4 stage: 256 K values, four v_mfma_scale_f32_32x32x64_f8f6f4.
+// In each 64-wide step lane half h holds elements [32h, 32h + 32) of its
+// weight row and of its band row: one MX block of either, whose E8M0 bytes it
+// passes. The matrix unit applies both scales, so the products go straight
+// into the fp32 accumulators (exact products of few-bit values: no promotion
+// and no partial sums as in the e4m3 stages). A row's eight scale bytes are
+// two dwords; shifted by 8 h, bytes 0 and 2 of a dword are the lane's scales
+// of two consecutive steps, which the instruction selects by itself.
+// Transposed accumulators as in the other stages. HALF: the K extent ends
+// after the first 128 values.
+template <int NMB, int NNB, bool HALF>
+__device__ __forceinline__ void compute_stage_w4a4(const lds_t* sa, const lds_t* sb, const lds_t* ss, int tid,
+                                                   f32x16 (&acc)[NMB][WaveGrid<NNB, OT_W4A4>::NCB]) {
+  using G = WaveGrid<NNB, OT_W4A4>;
+  const int lane = tid & 63, w = tid >> 6, wm = w % G::WM, wn = w / G::WM;
+  const int lr = lane & 31, hi = lane >> 5;
+  int sw[G::NCB][2], sx[NMB][2];
+#pragma unroll
+  for (int nb = 0; nb < G::NCB; ++nb)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      sw[nb][i] = *(const lds_i32*)(ss + kBM * 8 + wave_col<NNB, OT_W4A4>(nb / G::CPH, nb % G::CPH, wn, lr) * 8 + i * 4)
+                  >> (8 * hi);
+#pragma unroll
+  for (int mi = 0; mi < NMB; ++mi)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      sx[mi][i] = *(const lds_i32*)(ss + ((wm + G::WM * mi) * 32 + lr) * 8 + i * 4) >> (8 * hi);
+#pragma unroll
+  for (int ks = 0; ks < (HALF ? 2 : 4); ++ks) {
+    i32x8 fb[G::NCB], fa[NMB];
+#pragma unroll
+    for (int nb = 0; nb < G::NCB; ++nb) {
+      const i32x4 q =
+          *(const lds_i32x4*)(sb + lds_off<128>(wave_col<NNB, OT_W4A4>(nb / G::CPH, nb % G::CPH, wn, lr), ks * 2 + hi));
+      fb[nb] = i32x8{q[0], q[1], q[2], q[3], 0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int mi = 0; mi < NMB; ++mi) {
+      const i32x4 q = *(const lds_i32x4*)(sa + lds_off<128>((wm + G::WM * mi) * 32 + lr, ks * 2 + hi));
+      fa[mi] = i32x8{q[0], q[1], q[2], q[3], 0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int mi = 0; mi < NMB; ++mi)
+#pragma unroll
+      for (int nb = 0; nb < G::NCB; ++nb)
+        acc[mi][nb] = ks & 1 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[nb], fa[mi], acc[mi][nb], 4, 4, 2,
+                                                                               sw[nb][ks >> 1], 2, sx[mi][ks >> 1])
+                             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[nb], fa[mi], acc[mi][nb], 4, 4, 0,
+                                                                               sw[nb][ks >> 1], 0, sx[mi][ks >> 1]);
+  }
+}
+
 template <int MB, int NMB, int NNB, int OT>
 __device__ __forceinline__ void compute_any(const Tile& t, const lds_t* st, int kt, int tid,
                                             f32x16 (&acc)[NMB][WaveGrid<NNB, OT>::NCB]) {
-  if constexpr (mxfp4_weights(OT)) {
+  if constexpr (OT == OT_W4A4) {
+    const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
+    if (kslice(t, kt) == t.khalf) compute_stage_w4a4<NMB, NNB, true>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
+    else compute_stage_w4a4<NMB, NNB, false>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
+  } else if constexpr (mxfp4_weights(OT)) {
     const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     compute_stage_w4<NMB, NNB>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
   } else if constexpr (OT) {
@@ -604,7 +703,7 @@ __device__ __forceinline__ void compute_any(const Tile& t, const lds_t* st, int 
 // Whether a Linear-1 tile owns whole 128-column quantisation blocks of H
 // (e4m3 H, wide tiles) and stages them in LDS.
 template <int NNB, bool L1, int OT>
-constexpr bool stages_block_in_lds() { return OT && L1 && NNB * 32 == 128; }
+constexpr bool stages_block_in_lds() { return e4m3_acts(OT) && L1 && NNB * 32 == 128; }
 
 // The accumulators hold transposed blocks (the compute stages take the
 // weight rows as the MFMA's A operand), so lane l owns band row l % 32 of
@@ -646,7 +745,7 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& P, const Tile& t
   for (int mi = 0; mi < NMB; ++mi) {
     const int m = (wm + G::WM * mi) * 32 + lr;
     if (m >= t.rows) continue;
-    if constexpr (L1 && OT != OT_BF16) {
+    if constexpr (L1 && e4m3_acts(OT)) {
       // gate block c pairs with up block c of the second half: the same SwiGLU columns
       float* frow = P.Hf + (size_t)(t.row0 + m) * P.f + t.n * (NNB * 32);
 #pragma unroll
@@ -909,8 +1008,8 @@ __device__ __forceinline__ void tile_body(const GemmParams& P, const Tile& t0, l
   }
   lds_barrier();  // LDS ring free for the next tile
   if (P.trace) t_main = __builtin_amdgcn_s_memrealtime();
-  if constexpr (OT == OT_BF16 && MB <= 4) {
-    // the successor's first stages, if it has this tile's shape (the bf16
+  if constexpr (chains_tiles(OT) && MB <= 4) {
+    // the successor's first stages, if it has this tile's shape (this
     // epilogue leaves the LDS alone, so the ring is free from here on)
     if (ch.has_next) {
       const Tile& n0 = ch.next;
@@ -1097,7 +1196,7 @@ __device__ void quantize_block(const GemmParams& P, int row0, int rows, int j) {
 // needs no counting for Linear-2: its launch starts after this one ends.
 template <int OT>
 __device__ __forceinline__ void finish_l1_tile(const GemmParams& P, const Tile& t, int p, bool fused, lds_t* lds) {
-  if constexpr (!OT) {
+  if constexpr (!e4m3_acts(OT)) {
     if (fused) publish(P.l2_full + p, 1);
   } else {
     const int bn1 = t.nnb * 32;
@@ -1168,6 +1267,13 @@ __device__ __forceinline__ void record_tile(const GemmParams& P, bool l1, int p,
   }
 }
 
+// MXFP4 activations: 256 values of K per slice, the last slice half of one
+// where K is an odd multiple of 128.
+__device__ __forceinline__ void set_khalf(Tile& t, int K) {
+  t.ktiles = (K + 255) >> 8;
+  t.khalf = K & 128 ? t.ktiles - 1 : -1;
+}
+
 template <bool L1, int OT>
 __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int nnb) {
   constexpr int esz = OT ? 1 : 2;
@@ -1180,10 +1286,10 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
   t.nnb = nnb;
   t.cap_stride = P.cap;
   // weight rows: K elements of esz bytes, or K/2 bytes of packed MXFP4
-  constexpr bool W4 = mxfp4_weights(OT);
+  constexpr bool W4 = mxfp4_weights(OT) || OT == OT_W4A4;
   if constexpr (L1) {
     const int bn = nnb * 32;  // SwiGLU columns: bn gate rows and bn up rows
-    t.lda = (size_t)P.d * esz;
+    t.lda = OT == OT_W4A4 ? (size_t)P.d / 2 : (size_t)P.d * esz;
     t.ldb = W4 ? (size_t)P.d / 2 : (size_t)P.d * esz;
     // rows by t.arow: X row a_src[row0 + r] / k from X itself, or X_perm row
     // row0 + r from the band's first row
@@ -1195,8 +1301,10 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
     t.Bu = We + (size_t)(P.f + n * bn) * t.ldb;
     t.ktiles = P.d * esz / stage_k_bytes(OT);
     t.krot = 0;
+    if constexpr (OT == OT_W4A4) set_khalf(t, P.d);
     if constexpr (W4) {
       t.As = P.Xs + t.row0;
+      t.Ae = P.a_src ? P.Xe : P.Xe + (size_t)t.row0 * (P.d / 32);
       t.epitch = (size_t)P.d / 32;
       const uint8_t* Es = P.W1e + (size_t)e * 2 * P.f * t.epitch;
       t.Eg = Es + (size_t)(n * bn) * t.epitch;
@@ -1209,7 +1317,7 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
     }
   } else {
     const int bn = nnb * 64;  // output columns
-    t.lda = (size_t)P.f * esz;
+    t.lda = OT == OT_W4A4 ? (size_t)P.f / 2 : (size_t)P.f * esz;
     t.ldb = W4 ? (size_t)P.f / 2 : (size_t)P.f * esz;
     t.A = P.H + (size_t)t.row0 * t.lda;
     t.a_src = nullptr;
@@ -1217,9 +1325,11 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
     t.Bg = P.W2 + ((size_t)e * P.d + (size_t)n * bn) * t.ldb;
     t.Bu = t.Bg + (size_t)(bn / 2) * t.ldb;
     t.ktiles = P.f * esz / stage_k_bytes(OT);
+    if constexpr (OT == OT_W4A4) set_khalf(t, P.f);
     t.krot = (e * kKRot) % t.ktiles;
     if constexpr (W4) {
       t.As = P.Hs + t.row0;
+      t.Ae = P.He + (size_t)t.row0 * (P.f / 32);
       t.epitch = (size_t)P.f / 32;
       t.Eg = P.W2e + ((size_t)e * P.d + (size_t)n * bn) * t.epitch;
       t.Eu = t.Eg + (size_t)(bn / 2) * t.epitch;
@@ -1303,7 +1413,7 @@ __device__ __forceinline__ void separate_tiles(const GemmParams& P, int nb, int 
     coords(i, p, n, w);
     Chain ch;
     ch.pre = pre;
-    if (OT == OT_BF16 && i + G < end) {
+    if (chains_tiles(OT) && i + G < end) {
       int p2, n2, w2;
       coords(i + G, p2, n2, w2);
       ch.next = make_tile<L1, OT>(P, p2, n2, w2);
@@ -1326,6 +1436,11 @@ __global__ __launch_bounds__(gemm_threads(OT), 1) void moe_gemm_kernel(GemmParam
   const int Pb = P.meta[META_P];
   int p, n;
   Chain none;  // the fused schedules prefetch nothing across tiles
+  if constexpr (OT == OT_W4A4) {  // the two Linears are calls of their own
+    if (P.mode == MODE_SEP_L1) separate_tiles<true, OT>(P, Pb, P.N1, P.nnb1, lid, G, lds);
+    else separate_tiles<false, OT>(P, Pb, P.N2, P.nnb2, lid, G, lds);
+    return;
+  }
   switch (P.mode) {
     case MODE_SEP_L1:
       separate_tiles<true, OT>(P, Pb, P.N1, P.nnb1, lid, G, lds);

@@ -34,7 +34,9 @@ enum MetaSlot {
 // whole word when it starts (the workspace may hold anything before its first
 // use); inside moe_layer_forward the expert GEMM clears only its own bits, so
 // the dispatch's report survives until moe_check_workspace reads it.
-enum ArgErr { ARG_ERR_DISPATCH_CAP = 1, ARG_ERR_OFFSETS = 2, ARG_ERR_ROW_DST = 4, ARG_ERR_ALL = 7 };
+enum ArgErr {
+  ARG_ERR_DISPATCH_CAP = 1, ARG_ERR_OFFSETS = 2, ARG_ERR_ROW_DST = 4, ARG_ERR_ROW_SRC = 8, ARG_ERR_ALL = 15
+};
 
 // band_expert[p] of the band table: the band's local expert, plus
 // kBandSingle if the band is its expert's only one (the expert has at most
@@ -174,6 +176,17 @@ hipError_t launch_expert_forward_fused(const moe_problem_t& p, const Layout& L, 
                                        const int32_t* row_src, const float* X_perm_scale, const int32_t* row_dst,
                                        const void* W1, const void* W1_scale, const void* W2, const void* W2_scale,
                                        void* combine_buf, hipStream_t s);
+
+// The row-band plan of a call with its own offsets, row_src and row_dst
+// (either of the last two may be null), its row indices checked.
+hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
+                            const int32_t* row_src, const int32_t* row_dst, hipStream_t s);
+
+// One Linear on MXFP4 operands (validated arguments).
+hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const uint8_t* A,
+                               const uint8_t* A_scale, const int32_t* row_src, const int32_t* offsets,
+                               const int32_t* row_dst, const uint8_t* W, const uint8_t* W_scale, void* out,
+                               hipStream_t s);
 
 // Gradients of the combine (with the router's softmax) and of the dispatch
 // (validated arguments; see moe_combine_backward and moe_dispatch_backward).

@@ -194,7 +194,8 @@ typedef struct moe_workspace_layout {
                                             (MOE_FLAG_TILE_TRACE), meta[5] = device-side argument
                                             errors (bits: 1 = more local assignments than the row
                                             capacity, 2 = offsets not monotone or past the row
-                                            capacity, 4 = a row_dst outside the row capacity) */
+                                            capacity, 4 = a row_dst outside the row capacity,
+                                            8 = a row_src outside [0, T*k)) */
   size_t tile_trace;    /* moe_tile_record_t [tile_trace_capacity]; empty without MOE_FLAG_TILE_TRACE */
   size_t tile_trace_capacity;  /* records (a bound on the tiles of one call) */
   size_t total;         /* = moe_workspace_size */
@@ -466,6 +467,40 @@ MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows,
                                         uint8_t* scales, void* stream);
 MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                                           void* out, int out_fp32, void* stream);
+
+/* The experts' Linears with both operands in MXFP4 (W4A4): the tokens
+ * quantised by moe_mxfp4_quantize, the weights likewise (or as
+ * MOE_DTYPE_W4A8_MXFP4 takes them: the same format). Of p the shape, the row
+ * capacity, the flags and the grid are used; its dtype is not (offsets,
+ * row_src and row_dst may come from a dispatch of bf16 tokens), and the tiles
+ * run in the separate schedule's order. A layer forward is
+ *   moe_mxfp4_quantize(X) -> moe_mxfp4_linear1 -> moe_mxfp4_quantize(H)
+ *   -> moe_mxfp4_linear2 -> moe_combine.
+ *
+ * moe_mxfp4_linear1: X uint8 [T, d/2], X_scale uint8 [T, d/32] with row_src
+ * int32 [cap] (row r reads token row_src[r] / k), or, with row_src NULL,
+ * X uint8 [cap, d/2] and X_scale [cap, d/32] already in expert order; W1 uint8
+ * [E_l, 2f, d/2], W1_scale uint8 [E_l, 2f, d/32]. H bf16 [cap, f] out: row r =
+ * silu(g) * u of the fp32 products (g, u) = W1[e] x, rounded once.
+ *
+ * moe_mxfp4_linear2: H uint8 [cap, f/2], H_scale uint8 [cap, f/32] in expert
+ * order; W2 uint8 [E_l, d, f/2], W2_scale uint8 [E_l, d, f/32]. combine_buf
+ * [cap, d] out (fp32, or bf16 with MOE_FLAG_BF16_COMBINE_BUF): row row_dst[r] =
+ * W2[e] h.
+ *
+ * Rows past the last stay as they were. Products accumulate in fp32. Every
+ * array 16-byte aligned. Device-side checks, reported by moe_check_workspace as
+ * MOE_ERR_INVALID_ARGUMENT: offsets as in moe_expert_forward, row_src in
+ * [0, T*k), row_dst in [0, cap); if one fails nothing is computed and the
+ * output is left as it was. */
+MOE_API moe_status_t moe_mxfp4_linear1(const moe_problem_t* p, const uint8_t* X, const uint8_t* X_scale,
+                                       const int32_t* row_src, const int32_t* offsets, const uint8_t* W1,
+                                       const uint8_t* W1_scale, void* H, void* workspace, size_t ws_bytes,
+                                       void* stream);
+MOE_API moe_status_t moe_mxfp4_linear2(const moe_problem_t* p, const uint8_t* H, const uint8_t* H_scale,
+                                       const int32_t* offsets, const int32_t* row_dst, const uint8_t* W2,
+                                       const uint8_t* W2_scale, void* combine_buf, void* workspace, size_t ws_bytes,
+                                       void* stream);
 
 MOE_API const char* moe_status_string(moe_status_t s);
 MOE_API int moe_last_hip_error(void);

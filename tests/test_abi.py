@@ -220,3 +220,18 @@ def test_backward_and_codec_arguments_rejected_before_launch(L):
     assert L.moe_mxfp4_quantize(f, 0, 1, 32, odd, f, None) == 1
     assert L.moe_mxfp4_quantize(f, 0, 1, 32, f, None, None) == 1
     assert L.moe_mxfp4_dequantize(f, f, 1, 32, odd, 1, None) == 1
+
+
+def test_mxfp4_linear_arguments_rejected_before_launch(L):
+    p = moe.make_problem(**GOOD)
+    P, need = ctypes.byref(p), ctypes.c_size_t(moe.workspace_size(p))
+    f, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 4)   # never dereferenced
+    for fn, optional in ((L.moe_mxfp4_linear1, (2,)), (L.moe_mxfp4_linear2, ())):
+        for i in range(8):
+            if i in optional:
+                continue
+            assert fn(P, *[None if j == i else f for j in range(8)], need, None) == 1, i
+        assert fn(P, odd, *[f] * 7, need, None) == 1
+        assert fn(P, *[f] * 7, ctypes.c_void_p((1 << 20) + 16), need, None) == 1
+        assert fn(P, *[f] * 8, ctypes.c_size_t(need.value - 1), None) == 3
+        assert fn(None, *[f] * 8, need, None) == 1
