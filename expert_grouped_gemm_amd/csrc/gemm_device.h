@@ -444,15 +444,22 @@ __device__ __forceinline__ void fill_arow(Tile& t, int tid) {
 // whatever the tile width, schedule, grid or the order of the tokens.
 constexpr int kKRot = 5;
 
-// K slice streamed by pipeline stage kt of tile t.
+// K slice streamed by pipeline stage kt of tile t. A half slice (MXFP4
+// activations) is always the last stage: the others rotate among themselves.
+template <int OT>
 __device__ __forceinline__ int kslice(const Tile& t, int kt) {
+  if constexpr (OT == OT_W4A4) {
+    const int full = t.ktiles - (t.khalf >= 0 ? 1 : 0);
+    const int s = kt + t.krot;
+    return kt >= full ? kt : s >= full ? s - full : s;
+  }
   const int s = kt + t.krot;
   return s >= t.ktiles ? s - t.ktiles : s;
 }
 
 template <int MB, int NNB, int OT, bool NT>
 __device__ __forceinline__ void issue_stage(const Tile& t, int kt, lds_t* st, int tid) {
-  const int ks = kslice(t, kt);
+  const int ks = kslice<OT>(t, kt);
 #pragma unroll
   for (int j = 0; j < stage_loads(MB, NNB, OT); ++j) issue_load<MB, NNB, OT, NT>(t, ks, st, tid, j);
 }
@@ -635,10 +642,14 @@ __device__ __forceinline__ void compute_stage_w4(const lds_t* sa, const lds_t* s
 // and no partial sums as in the e4m3 stages). A row's eight scale bytes are
 // two dwords; shifted by 8 h, bytes 0 and 2 of a dword are the lane's scales
 // of two consecutive steps, which the instruction selects by itself.
-// Transposed accumulators as in the other stages. HALF: the K extent ends
-// after the first 128 values.
-template <int NMB, int NNB, bool HALF>
+// Transposed accumulators as in the other stages. LAST: the stage may be the
+// half slice (the K extent ends after its first 128 values), which kslice
+// puts last: only there does a branch stand between the MFMAs. (With the
+// choice in every stage the compiler kept two sets of accumulators and
+// spilled.)
+template <int NMB, int NNB, bool LAST>
 __device__ __forceinline__ void compute_stage_w4a4(const lds_t* sa, const lds_t* sb, const lds_t* ss, int tid,
+                                                   bool half_slice,
                                                    f32x16 (&acc)[NMB][WaveGrid<NNB, OT_W4A4>::NCB]) {
   using G = WaveGrid<NNB, OT_W4A4>;
   const int lane = tid & 63, w = tid >> 6, wm = w % G::WM, wn = w / G::WM;
@@ -656,7 +667,8 @@ __device__ __forceinline__ void compute_stage_w4a4(const lds_t* sa, const lds_t*
     for (int i = 0; i < 2; ++i)
       sx[mi][i] = *(const lds_i32*)(ss + ((wm + G::WM * mi) * 32 + lr) * 8 + i * 4) >> (8 * hi);
 #pragma unroll
-  for (int ks = 0; ks < (HALF ? 2 : 4); ++ks) {
+  for (int ks = 0; ks < 4; ++ks) {
+    if (LAST && ks == 2 && half_slice) break;
     i32x8 fb[G::NCB], fa[NMB];
 #pragma unroll
     for (int nb = 0; nb < G::NCB; ++nb) {
@@ -680,13 +692,14 @@ __device__ __forceinline__ void compute_stage_w4a4(const lds_t* sa, const lds_t*
   }
 }
 
-template <int MB, int NMB, int NNB, int OT>
+// LAST: the tile's last stage (the others' code does not depend on it, except
+// for MXFP4 activations).
+template <int MB, int NMB, int NNB, int OT, bool LAST = false>
 __device__ __forceinline__ void compute_any(const Tile& t, const lds_t* st, int kt, int tid,
                                             f32x16 (&acc)[NMB][WaveGrid<NNB, OT>::NCB]) {
   if constexpr (OT == OT_W4A4) {
     const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
-    if (kslice(t, kt) == t.khalf) compute_stage_w4a4<NMB, NNB, true>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
-    else compute_stage_w4a4<NMB, NNB, false>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
+    compute_stage_w4a4<NMB, NNB, LAST>(st, st + stage_a_bytes(MB, OT), ss, tid, t.khalf >= 0, acc);
   } else if constexpr (mxfp4_weights(OT)) {
     const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     compute_stage_w4<NMB, NNB>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
@@ -899,7 +912,7 @@ __device__ __forceinline__ void drain(const Tile& t, lds_t* lds, int rd, int kt,
   constexpr int S = ring_stages(MB, NNB, OT), SB = stage_bytes(MB, NNB, OT);
   wait_vmcnt<R * stage_loads(MB, NNB, OT)>();
   lds_barrier();
-  if constexpr (NMB > 0) compute_any<MB, NMB, NNB, OT>(t, lds + rd * SB, kt, tid, acc);
+  if constexpr (NMB > 0) compute_any<MB, NMB, NNB, OT, R == 0>(t, lds + rd * SB, kt, tid, acc);
   if constexpr (R > 0) drain<MB, NMB, NNB, OT, R - 1>(t, lds, rd + 1 == S ? 0 : rd + 1, kt + 1, tid, acc);
 }
 
@@ -966,8 +979,12 @@ __device__ __forceinline__ void tile_body(const GemmParams& P, const Tile& t0, l
     }
     wait_vmcnt<0>();
     lds_barrier();
-    if constexpr (NMB > 0)
+    if constexpr (NMB > 0 && OT == OT_W4A4) {
+      for (int kt = 0; kt < KT - 1; ++kt) compute_any<MB, NMB, NNB, OT>(t, lds + kt * SB, kt, tid, acc);
+      compute_any<MB, NMB, NNB, OT, true>(t, lds + (KT - 1) * SB, KT - 1, tid, acc);
+    } else if constexpr (NMB > 0) {
       for (int kt = 0; kt < KT; ++kt) compute_any<MB, NMB, NNB, OT>(t, lds + kt * SB, kt, tid, acc);
+    }
   } else {
     if constexpr (loader) {
       if (!ch.pre) {
@@ -987,7 +1004,7 @@ __device__ __forceinline__ void tile_body(const GemmParams& P, const Tile& t0, l
       wait_vmcnt<(S - 2) * LD>();  // a loader's loads of stage kt have landed
       lds_barrier();               // ... every loader's
       if constexpr (loader) {
-        const int ks = kslice(t, kt + S - 1);
+        const int ks = kslice<OT>(t, kt + S - 1);
         lds_t* st = lds + wr * SB;
         if constexpr (NMB > 0 && OT == OT_BF16) {
           compute_stage<NMB, NNB, LD>(lds + rd * SB, lds + rd * SB + stage_a_bytes(MB, OT), tid, acc,
@@ -1326,7 +1343,8 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
     t.Bu = t.Bg + (size_t)(bn / 2) * t.ldb;
     t.ktiles = P.f * esz / stage_k_bytes(OT);
     if constexpr (OT == OT_W4A4) set_khalf(t, P.f);
-    t.krot = (e * kKRot) % t.ktiles;
+    if constexpr (OT == OT_W4A4) t.krot = t.ktiles > 1 ? (e * kKRot) % (t.ktiles - (t.khalf >= 0 ? 1 : 0)) : 0;
+    else t.krot = (e * kKRot) % t.ktiles;
     if constexpr (W4) {
       t.As = P.Hs + t.row0;
       t.Ae = P.He + (size_t)t.row0 * (P.f / 32);
