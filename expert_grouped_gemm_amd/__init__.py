@@ -20,7 +20,8 @@ __all__ = [
     "MoEError", "Problem", "WorkspaceLayout", "lib", "make_problem", "workspace_size", "workspace_layout",
     "workspace_views", "route_topk", "dispatch", "dispatch_noalloc", "expert_forward", "combine", "layer_forward",
     "check_workspace", "tile_trace", "schedule_of", "store_burst_probe", "owner_plan", "owner_gather",
-    "segment_copy", "expert_forward_signal", "segment_copy_wait", "combine_backward", "dispatch_backward",
+    "segment_copy", "expert_forward_signal", "segment_copy_wait", "combine_backward", "expert_backward",
+    "dispatch_backward", "backward_workspace_size", "alloc_backward_workspace",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear1", "mxfp4_linear2", "SCHED", "DTYPE", "STATUS",
 ]
 
@@ -123,6 +124,10 @@ def lib() -> ctypes.CDLL:
         L.moe_mxfp4_quantize.argtypes = [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]
         L.moe_mxfp4_dequantize.restype = ctypes.c_int
         L.moe_mxfp4_dequantize.argtypes = [_P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P]
+        L.moe_backward_workspace_size.restype = ctypes.c_size_t
+        L.moe_backward_workspace_size.argtypes = [PP]
+        L.moe_expert_backward.restype = ctypes.c_int
+        L.moe_expert_backward.argtypes = [PP] + [_P] * 11 + [ctypes.c_size_t, _P]
         for name in ("moe_mxfp4_linear1", "moe_mxfp4_linear2"):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [PP] + [_P] * 8 + [ctypes.c_size_t, _P]
@@ -399,6 +404,35 @@ def combine_backward(p: Problem, dY, combine_buf, tok_off, topk_idx, topk_w, d_c
             _operand(w, "d_logits", d_logits, torch.float32, p.T * p.E_global, optional=True))
     with _On(w, stream, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf, d_topk_w, d_logits) as s:
         _check(lib().moe_combine_backward(ctypes.byref(p), *args, s), "moe_combine_backward")
+
+
+def backward_workspace_size(p: Problem) -> int:
+    """Bytes of a workspace for expert_backward (which serves the forward calls too)."""
+    n = lib().moe_backward_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise MoEError(2, "moe_backward_workspace_size")
+    return n
+
+
+def alloc_backward_workspace(p: Problem, device="cuda") -> torch.Tensor:
+    return torch.empty(backward_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def expert_backward(p: Problem, X, row_src, offsets, row_dst, W1, W2, d_combine_buf, d_x_slots, dW1, dW2, workspace,
+                    stream=None):
+    """moe_expert_backward: the gradients of the experts' rows (into their
+    slots) and weights from the gradient of the combine buffer. X holds the
+    tokens with row_src, or the rows in expert order with row_src=None."""
+    w, bf, cap, El = "expert_backward", torch.bfloat16, row_capacity(p), p.e_end - p.e_begin
+    args = (_operand(w, "X", X, bf, (cap if row_src is None else p.T) * p.d),
+            _operand(w, "row_src", row_src, torch.int32, cap, optional=True),
+            _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
+            _operand(w, "W1", W1, bf, El * 2 * p.f * p.d), _operand(w, "W2", W2, bf, El * p.d * p.f),
+            _operand(w, "d_combine_buf", d_combine_buf, bf, cap * p.d),
+            _operand(w, "d_x_slots", d_x_slots, bf, cap * p.d), _operand(w, "dW1", dW1, bf, El * 2 * p.f * p.d),
+            _operand(w, "dW2", dW2, bf, El * p.d * p.f), _operand(w, "workspace", workspace, torch.uint8, 0))
+    with _On(w, stream, X, row_src, offsets, row_dst, W1, W2, d_combine_buf, d_x_slots, dW1, dW2, workspace) as s:
+        _check(lib().moe_expert_backward(ctypes.byref(p), *args, workspace.numel(), s), "moe_expert_backward")
 
 
 def dispatch_backward(p: Problem, d_x_slots, tok_off, dX, dX_fp32=None, stream=None):

@@ -389,6 +389,33 @@ MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
 
+MOE_API size_t moe_backward_workspace_size(const moe_problem_t* p) {
+  if (check_problem(p) != MOE_OK || p->dtype != MOE_DTYPE_BF16) return 0;
+  return moe::backward_layout(*p, moe::make_layout(*p)).total;
+}
+
+MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, const int32_t* row_src,
+                                         const int32_t* offsets, const int32_t* row_dst, const void* W1,
+                                         const void* W2, const void* d_combine_buf, void* d_x_slots, void* dW1,
+                                         void* dW2, void* workspace, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!X || !offsets || !row_dst || !W1 || !W2 || !d_combine_buf || !d_x_slots || !dW1 || !dW2)
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {X, W1, W2, d_combine_buf, (const void*)d_x_slots, (const void*)dW1, (const void*)dW2})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARGUMENT;
+  // the inputs are read until the last launch
+  for (const void* in : {X, W1, W2, d_combine_buf})
+    if (in == d_x_slots || in == dW1 || in == dW2) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  if (ws_bytes < moe::backward_layout(*p, L).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const hipError_t e = moe::launch_expert_backward(*p, L, static_cast<char*>(workspace), X, row_src, offsets, row_dst,
+                                                   W1, W2, d_combine_buf, d_x_slots, dW1, dW2, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
 MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d_x_slots, const int32_t* tok_off,
                                            void* dX, float* dX_fp32, void* stream) {
   moe_status_t st = check_problem(p);

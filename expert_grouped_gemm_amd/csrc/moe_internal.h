@@ -182,6 +182,19 @@ hipError_t launch_expert_forward_fused(const moe_problem_t& p, const Layout& L, 
 hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
                             const int32_t* row_src, const int32_t* row_dst, hipStream_t s);
 
+// moe_expert_backward's intermediates, behind the workspace's own regions.
+struct BackwardLayout {
+  size_t gu;    // fp32 [cap, 2f]  gate and up
+  size_t act;   // bf16 [cap, f]   SwiGLU output
+  size_t dh;    // bf16 [cap, 2f]  gradients of gate and up
+  size_t total;
+};
+BackwardLayout backward_layout(const moe_problem_t& p, const Layout& L);
+hipError_t launch_expert_backward(const moe_problem_t& p, const Layout& L, char* ws, const void* X,
+                                  const int32_t* row_src, const int32_t* offsets, const int32_t* row_dst,
+                                  const void* W1, const void* W2, const void* dO, void* dxs, void* dW1, void* dW2,
+                                  hipStream_t s);
+
 // One Linear on MXFP4 operands (validated arguments).
 hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const uint8_t* A,
                                const uint8_t* A_scale, const int32_t* row_src, const int32_t* offsets,

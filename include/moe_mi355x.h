@@ -449,6 +449,38 @@ MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY
 MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d_x_slots, const int32_t* tok_off,
                                            void* dX, float* dX_fp32, void* stream);
 
+/* Gradient of the experts' products (moe_expert_forward, bf16), between the
+ * two above: a backward pass of the share is moe_combine_backward ->
+ * moe_expert_backward -> moe_dispatch_backward on the forward call's
+ * topk_idx, topk_w, offsets, row_src, row_dst, tok_off and combine buffer.
+ *   X, row_src   bf16 [T, d] tokens with row_src int32 [cap] (row r reads token
+ *                row_src[r] / k), or, with row_src NULL, the rows themselves in
+ *                expert order, [cap, d] (X_perm, or the padded rows of
+ *                moe_owner_gather)
+ *   offsets, row_dst   as for moe_expert_forward; no two rows may share a slot
+ *   W1, W2       as for moe_expert_forward
+ *   d_combine_buf bf16 [cap, d]   the gradient of row r at slot row_dst[r]
+ * Outputs, all of them written whole and none of them added to:
+ *   d_x_slots bf16 [cap, d]       the gradient of row r's token values, at slot
+ *                                 row_dst[r]; slots of no row stay as they were
+ *   dW1 bf16 [E_l, 2f, d], dW2 bf16 [E_l, d, f]; 0 for an expert without rows
+ * The SwiGLU inputs are recomputed in fp32; the SwiGLU output (as in the
+ * forward) and the gradients of gate and up are rounded to bf16, being
+ * operands of products; sums are fp32 and each output is rounded once. The
+ * same call gives the same bits.
+ * bf16 only (MOE_ERR_UNSUPPORTED otherwise). The workspace is one of
+ * moe_backward_workspace_size(p) bytes (0 for an invalid or non-bf16
+ * problem): a workspace of moe_workspace_size(p) with this call's
+ * intermediates behind it, so it serves the forward calls too; of their
+ * regions this call writes only meta and the row-band tables. Inputs may not be
+ * outputs. Device-side checks as in moe_mxfp4_linear1 (offsets, row_src,
+ * row_dst): if one fails no output is written. */
+MOE_API size_t moe_backward_workspace_size(const moe_problem_t* p);
+MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, const int32_t* row_src,
+                                         const int32_t* offsets, const int32_t* row_dst, const void* W1,
+                                         const void* W2, const void* d_combine_buf, void* d_x_slots, void* dW1,
+                                         void* dW2, void* workspace, size_t ws_bytes, void* stream);
+
 /* MXFP4 codec (OCP MXFP4: E2M1 elements, two per byte, the even element in
  * the low nibble; one E8M0 scale byte per 32 consecutive elements of a row).
  * x [rows, cols], cols % 32 == 0, rows >= 0, DEVICE memory; codes uint8

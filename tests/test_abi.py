@@ -235,3 +235,26 @@ def test_mxfp4_linear_arguments_rejected_before_launch(L):
         assert fn(P, *[f] * 7, ctypes.c_void_p((1 << 20) + 16), need, None) == 1
         assert fn(P, *[f] * 8, ctypes.c_size_t(need.value - 1), None) == 3
         assert fn(None, *[f] * 8, need, None) == 1
+
+
+def test_expert_backward_arguments_rejected_before_launch(L):
+    p = moe.make_problem(**GOOD)
+    P, need = ctypes.byref(p), ctypes.c_size_t(moe.backward_workspace_size(p))
+    assert need.value > moe.workspace_size(p)
+    f = [ctypes.c_void_p((1 + i) << 20) for i in range(11)]    # never dereferenced
+    for i in range(11):
+        if i != 1:                                             # row_src may be NULL
+            assert L.moe_expert_backward(P, *[None if j == i else x for j, x in enumerate(f)], need, None) == 1, i
+    for i in (0, 4, 5, 6, 7, 8, 9):
+        args = [ctypes.c_void_p(x.value + 8) if j == i else x for j, x in enumerate(f)]
+        assert L.moe_expert_backward(P, *args, need, None) == 1, i
+    for i in (7, 8, 9):                                        # an output that is an input
+        for j in (0, 4, 5, 6):
+            args = list(f)
+            args[i] = f[j]
+            assert L.moe_expert_backward(P, *args, need, None) == 1, (i, j)
+    assert L.moe_expert_backward(P, *f, ctypes.c_size_t(need.value - 1), None) == 3
+    for dtype in ("fp8_e4m3", "w4a8_mxfp4"):
+        q = moe.make_problem(128, 128, 256, 4, 2, dtype=dtype)
+        assert L.moe_backward_workspace_size(ctypes.byref(q)) == 0
+        assert L.moe_expert_backward(ctypes.byref(q), *f, need, None) == 2
