@@ -29,7 +29,9 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 
 enum BwdOp { BWD_GU = 0, BWD_DACT = 1, BWD_DX = 2, BWD_DW2 = 3, BWD_DW1 = 4 };
 __host__ __device__ constexpr bool p_strided(int OP) { return OP != BWD_GU; }
@@ -38,8 +40,12 @@ __host__ __device__ constexpr bool q_strided(int OP) { return OP >= BWD_DW2; }
 constexpr int kBK = 64;                      // K values per stage
 constexpr int kTP = 256;                     // columns (P side) of a tile
 constexpr int kBwdThreads = 512;             // 8 wavefronts: 2 (Q) x 4 (P)
+constexpr int kLoaders = 4;                  // the last 4 (one per SIMD) issue the ring's loads
 constexpr int kStageP = kTP * kBK * 2;       // bytes of the P operand in a stage
-constexpr int kStageQ = kBM * kBK * 2;
+
+// QB: 32-row blocks of the Q side of a tile (4 or 8).
+__host__ __device__ constexpr int stage_q(int QB) { return QB * 32 * kBK * 2; }
+__host__ __device__ constexpr int bwd_ring(int QB) { return kGemmLds / (kStageP + stage_q(QB)); }
 
 struct BwdParams {
   const uint8_t* X;          // token rows [T, d] (through row_src) or expert-ordered rows
@@ -75,37 +81,87 @@ struct Side {
   int div;
 };
 
-__device__ __forceinline__ int side_row(const Side& s, int r) {
-  r = min(r, s.valid - 1);
-  return s.idx ? s.idx[r] / s.div : r;
-}
-
 // Column-chunk swizzle of a KS stage: the four K rows a transposing read takes
 // go to the four 64-byte quarters of a bank line.
 __device__ __forceinline__ int ks_swizzle(int kk) { return (kk & 3) << 2; }
 
-// Stage kt of one side into st: ROWS rows of 128 bytes (KC), or 64 K rows of
-// 512 bytes (KS). Rows past the valid ones re-read the last.
-template <bool KS, int ROWS>
-__device__ __forceinline__ void issue_side(const Side& s, int kt, lds_t* st, int w, int lane) {
-  if constexpr (KS) {
+// The ring's loads of one side, as one loader wavefront issues them: NI
+// instructions of 1 KiB per stage. An instruction takes 8 rows of 128 bytes
+// (KC) or 2 K rows of 512 (KS); loader lw of 4 takes instructions 4 j + lw, so
+// its lanes' rows advance by a uniform step from one to the next (and the
+// swizzle, which depends on the row modulo 16 or 4, not at all): the address is
+// a uniform base plus one 32-bit lane offset.
+template <bool KS, int NI>
+struct Loads {
+  const uint8_t* base;
+  uint32_t pitch, lane_off;
+  const int32_t* idx;
+  int div, valid;
+  uint32_t row_off[KS ? 1 : NI];  // KC with rows of their own places
+  bool direct;
+  int next;                       // KS through idx: this lane's K row of the next stage to issue
+
+  __device__ __forceinline__ void init(const Side& s, int lw, int lane, bool plain_rows) {
+    base = s.base;
+    pitch = s.pitch;
+    idx = s.idx;
+    div = s.div;
+    valid = s.valid;
+    direct = plain_rows;
+    if constexpr (KS) {
+      const int kk = 2 * lw + (lane >> 5);
+      lane_off = (((lane & 31) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
+      direct = idx == nullptr;
+      next = idx && valid > 0 ? idx[min(lane, valid - 1)] / div : 0;
+    } else {
+      const int r = lw * 8 + (lane >> 3);
+      const uint32_t chunk = ((lane & 7) ^ chunk_swizzle<128>(r)) << 4;
+      lane_off = direct ? r * pitch + chunk : chunk;
+      if (!direct) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = j * 8 + w, kk = 2 * i + (lane >> 5);
-      const int chunk = ((lane & 31) ^ ks_swizzle(kk)) & (s.chunks - 1);
-      const uint8_t* g = s.base + (size_t)side_row(s, kt * kBK + kk) * s.pitch + (chunk << 4);
-      __builtin_amdgcn_global_load_lds(g, st + i * 1024, 16, 0, 0);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < ROWS / 64; ++j) {
-      const int i = j * 8 + w, r = i * 8 + (lane >> 3);
-      const int chunk = (lane & 7) ^ chunk_swizzle<128>(r);
-      const uint8_t* g = s.base + (size_t)side_row(s, r) * s.pitch + kt * 128 + (chunk << 4);
-      __builtin_amdgcn_global_load_lds(g, st + i * 1024, 16, 0, 0);
+        for (int j = 0; j < NI; ++j) {
+          const int row = min(j * 32 + r, valid - 1);
+          row_off[j] = (uint32_t)(idx ? idx[row] / div : row) * pitch;
+        }
+      }
     }
   }
-}
+
+  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
+    if constexpr (KS) {
+      const int left = valid - kt * kBK;
+      if (direct && left >= kBK) {
+        const uint8_t* b0 = base + (size_t)kt * kBK * pitch;
+        const uint32_t off = (uint32_t)(2 * lw + (lane >> 5)) * pitch + lane_off;
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          __builtin_amdgcn_global_load_lds(b0 + (size_t)j * 8 * pitch + off, st + (4 * j + lw) * 1024, 16, 0, 0);
+      } else {
+        // K row kk of the stage is row `rows` of lane kk: through idx (fetched
+        // when the stage before was issued), or, in a last, partial stage,
+        // rows past the end re-reading the last (they are zeroed in the LDS)
+        const int rows = direct ? kt * kBK + min(lane, left - 1) : next;
+        if (!direct) next = idx[min((kt + 1) * kBK + lane, valid - 1)] / div;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          const int r0 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw);
+          const int r1 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw + 1);
+          const uint8_t* g = base + (size_t)(lane < 32 ? r0 : r1) * pitch + lane_off;
+          __builtin_amdgcn_global_load_lds(g, st + (4 * j + lw) * 1024, 16, 0, 0);
+        }
+      }
+    } else {
+      const uint8_t* b0 = base + (size_t)kt * 128;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        // columns that do not exist (a 128-wide tile) re-read the first ones
+        const uint8_t* bj = direct ? b0 + (size_t)(j * 32 < valid ? j : j - NI / 2) * 32 * pitch : b0;
+        const uint32_t off = direct ? lane_off : row_off[j] + lane_off;
+        __builtin_amdgcn_global_load_lds(bj + off, st + (4 * j + lw) * 1024, 16, 0, 0);
+      }
+    }
+  }
+};
 
 // Fragment of the 16 K values of step ks and the 32 rows / columns of block
 // blk: lane l holds row blk * 32 + l % 32, K values 8 (l / 32) .. + 7.
@@ -124,9 +180,8 @@ __device__ __forceinline__ bf16x8 fragment(const lds_t* st, int blk, int ks, int
   }
 }
 
-__device__ __forceinline__ uint2 pack4(const float (&v)[4]) {
-  return make_uint2((uint32_t)f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
-                    (uint32_t)f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
 }
 
 // A tile: where its operands are and where its results go.
@@ -140,46 +195,117 @@ struct BwdTile {
   int cols;     // valid output columns (128 or 256)
 };
 
+// The results of one 32-row block of a wavefront (its 64 columns), through the
+// wavefront's own 8 KiB of the free ring: a lane of the accumulator holds 4
+// consecutive columns of a row, whose direct store would write 8 or 16 bytes
+// into each of 32 rows; read back, every store writes whole 128-byte lines of
+// few rows. m0: the block's first row; dst: this lane's output row of block
+// row lane % 32 (DX: its slot).
 template <int OP>
-__device__ __forceinline__ void store_tile(const BwdParams& P, const BwdTile& t, int m, int c, const float (&v)[4]) {
-  const size_t row = (size_t)t.row0 + m;
-  const int col = t.col0 + c;
-  if constexpr (OP == BWD_GU) {
-    *reinterpret_cast<float4*>(P.GU + row * (2 * (size_t)P.f) + col) = make_float4(v[0], v[1], v[2], v[3]);
-  } else if constexpr (OP == BWD_DACT) {
-    const float* gu = P.GU + row * (2 * (size_t)P.f) + col;
-    const float4 g4 = *reinterpret_cast<const float4*>(gu), u4 = *reinterpret_cast<const float4*>(gu + P.f);
-    const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-    float a[4], dg[4], du[4];
+__device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t, lds_t* wl, const f32x16 (&acc)[2],
+                                            int m0, int c0, int dst, int lane) {
+  const int lr = lane & 31, hi = lane >> 5;
+  if constexpr (OP == BWD_GU || OP == BWD_DACT) {
+    // 32 rows of 256 bytes (fp32), 16-byte chunks swizzled by row
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g[i] * -1.4426950408889634f));
-      const float gs = g[i] * s;
-      a[i] = gs * u[i];
-      du[i] = v[i] * gs;
-      dg[i] = v[i] * u[i] * (s + gs * (1.0f - s));
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(lds_f32x4*)(wl + lr * 256 + (((b * 8 + 2 * q + hi) ^ (lr & 15)) << 4)) =
+            f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+    wave_lds_sync();
+    const int c = lane & 15;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = j * 4 + (lane >> 4);
+      const f32x4 v = *(const lds_f32x4*)(wl + r * 256 + ((c ^ (r & 15)) << 4));
+      if (m0 + r >= t.rows) continue;
+      const size_t row = (size_t)t.row0 + m0 + r;
+      const int col = t.col0 + c0 + c * 4;
+      if constexpr (OP == BWD_GU) {
+        *reinterpret_cast<float4*>(P.GU + row * (2 * (size_t)P.f) + col) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        const float* gu = P.GU + row * (2 * (size_t)P.f) + col;
+        const float4 g4 = *reinterpret_cast<const float4*>(gu), u4 = *reinterpret_cast<const float4*>(gu + P.f);
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+        float a[4], dg[4], du[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g[i] * -1.4426950408889634f));
+          const float gs = g[i] * s;
+          a[i] = gs * u[i];
+          du[i] = v[i] * gs;
+          dg[i] = v[i] * u[i] * (s + gs * (1.0f - s));
+        }
+        *reinterpret_cast<uint2*>(P.act + row * P.f + col) = make_uint2(pack2(a[0], a[1]), pack2(a[2], a[3]));
+        uint16_t* dh = P.dH + row * (2 * (size_t)P.f) + col;
+        *reinterpret_cast<uint2*>(dh) = make_uint2(pack2(dg[0], dg[1]), pack2(dg[2], dg[3]));
+        *reinterpret_cast<uint2*>(dh + P.f) = make_uint2(pack2(du[0], du[1]), pack2(du[2], du[3]));
+      }
     }
-    *reinterpret_cast<uint2*>(P.act + row * P.f + col) = pack4(a);
-    uint16_t* dh = P.dH + row * (2 * (size_t)P.f) + col;
-    *reinterpret_cast<uint2*>(dh) = pack4(dg);
-    *reinterpret_cast<uint2*>(dh + P.f) = pack4(du);
-  } else if constexpr (OP == BWD_DX) {
-    *reinterpret_cast<uint2*>(P.dxs + (size_t)P.row_dst[row] * P.d + col) = pack4(v);
-  } else if constexpr (OP == BWD_DW2) {
-    *reinterpret_cast<uint2*>(P.dW2 + ((size_t)t.e * P.d + row) * P.f + col) = pack4(v);
   } else {
-    *reinterpret_cast<uint2*>(P.dW1 + ((size_t)t.e * 2 * P.f + row) * P.d + col) = pack4(v);
+    // 32 rows of 128 bytes (bf16)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(lds_u32x2*)(wl + lr * 128 + (((b * 4 + q) ^ (lr & 7)) << 4) + hi * 8) =
+            u32x2{pack2(acc[b][4 * q], acc[b][4 * q + 1]), pack2(acc[b][4 * q + 2], acc[b][4 * q + 3])};
+    wave_lds_sync();
+    const int c = lane & 7;
+    const size_t ld = OP == BWD_DW2 ? P.f : P.d;
+    uint16_t* out = OP == BWD_DX    ? P.dxs
+                    : OP == BWD_DW2 ? P.dW2 + (size_t)t.e * P.d * P.f
+                                    : P.dW1 + (size_t)t.e * 2 * P.f * P.d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = j * 8 + (lane >> 3);
+      const i32x4 v = *(const lds_i32x4*)(wl + r * 128 + ((c ^ (r & 7)) << 4));
+      const size_t row = OP == BWD_DX ? (size_t)__shfl(dst, r, 64) : (size_t)t.row0 + m0 + r;
+      if (m0 + r < t.rows) *reinterpret_cast<i32x4*>(out + row * ld + t.col0 + c0 + c * 8) = v;
+    }
+  }
+  wave_lds_sync();
+}
+
+// One stage: MFMAs of a wavefront that owns Q blocks wq, wq + 2, ... and the
+// two P blocks from 2 wp on. The fragments of step ks + 1 are read before the
+// MFMAs of step ks.
+template <bool PS, bool QS, int NM, class Issue>
+__device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int lane, f32x16 (&acc)[NM][2],
+                                          const Issue& issue) {
+  bf16x8 fp[2][2], fq[2][NM];
+  auto read = [&](int ks, int buf) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) fp[buf][b] = fragment<PS>(st, 2 * wp + b, ks, lane);
+#pragma unroll
+    for (int a = 0; a < NM; ++a) fq[buf][a] = fragment<QS>(st + kStageP, wq + 2 * a, ks, lane);
+  };
+  read(0, 0);
+#pragma unroll
+  for (int ks = 0; ks < kBK / 16; ++ks) {
+    if (ks + 1 < kBK / 16) read(ks + 1, (ks + 1) & 1);
+    if (ks == 0) issue();
+#pragma unroll
+    for (int a = 0; a < NM; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[ks & 1][b], fq[ks & 1][a], acc[a][b], 0, 0, 0);
   }
 }
 
-// QB: 32-row blocks of the Q side (4 or 8). Each wavefront owns QB / 2 of
-// them and 2 of the 8 column blocks.
-template <int OP, int QB>
-__device__ __forceinline__ void run_bwd_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
+// One tile. A ring of bwd_ring(QB) stages in the LDS, one barrier per stage:
+// it shows the stage complete (each loader has waited for its own loads) and
+// every wavefront done with the slot the loaders refill next.
+template <int OP, int QB, bool LOADER>
+__device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile& t, lds_t* lds) {
   constexpr bool PS = p_strided(OP), QS = q_strided(OP);
-  constexpr int NM = QB / 2, LD = 4 + (QS ? 4 : QB / 2);
-  constexpr int SB = kStageP + kStageQ;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wq = w & 1, wp = w >> 1;
+  constexpr int NM = QB / 2, NIQ = QS ? 8 : QB, LD = 8 + NIQ;
+  constexpr int S = bwd_ring(QB), SB = kStageP + stage_q(QB);
+  static_assert(!QS || QB == 8, "a strided Q side has 256 columns");
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w & 1, wp = w >> 1, lw = w - 4;
   f32x16 acc[NM][2];
 #pragma unroll
   for (int a = 0; a < NM; ++a)
@@ -188,64 +314,70 @@ __device__ __forceinline__ void run_bwd_tile(const BwdParams& P, const BwdTile& 
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
 
-  auto issue = [&](int kt) {
-    lds_t* st = lds + (kt & 1) * SB;
-    issue_side<PS, kTP>(t.P, kt, st, w, lane);
-    issue_side<QS, QB * 32>(t.Q, kt, st + kStageP, w, lane);
+  const int KT = t.ktiles;
+  Loads<PS, 8> lp;
+  Loads<QS, NIQ> lq;
+  auto issue = [&](int kt, int slot) {
+    lp.issue(kt, lds + slot * SB, lw, lane);
+    lq.issue(kt, lds + slot * SB + kStageP, lw, lane);
   };
-  if (t.ktiles > 0) issue(0);
-  for (int kt = 0; kt < t.ktiles; ++kt) {
-    if (kt + 1 < t.ktiles) {
-      issue(kt + 1);
-      wait_vmcnt<LD>();
-    } else {
-      wait_vmcnt<0>();
+  if constexpr (LOADER) {
+    lp.init(t.P, lw, lane, true);
+    lq.init(t.Q, lw, lane, false);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+      if (s < KT) issue(s, s);
+  }
+  int rd = 0, wr = S - 1;
+  for (int kt = 0; kt < KT; ++kt) {
+    if constexpr (LOADER) {
+      if (S > 2 && kt + 1 < KT) wait_vmcnt<(S - 2) * LD>();
+      else wait_vmcnt<0>();
     }
     lds_barrier();
-    lds_t* st = lds + (kt & 1) * SB;
+    lds_t* st = lds + rd * SB;
     if constexpr (QS) {
       // K rows past the expert's last: zero on both sides
       const int left = t.P.valid - kt * kBK;
       if (left < kBK) {
-        for (int i = left * 32 + (int)threadIdx.x; i < kBK * 32; i += kBwdThreads) {
+        for (int i = left * 32 + tid; i < kBK * 32; i += kBwdThreads) {
           *(lds_i32x4*)(st + i * 16) = i32x4{0, 0, 0, 0};
           *(lds_i32x4*)(st + kStageP + i * 16) = i32x4{0, 0, 0, 0};
         }
         lds_barrier();
       }
     }
-#pragma unroll
-    for (int ks = 0; ks < kBK / 16; ++ks) {
-      bf16x8 fp[2], fq[NM];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) fp[b] = fragment<PS>(st, wp + 4 * b, ks, lane);
-#pragma unroll
-      for (int a = 0; a < NM; ++a) fq[a] = fragment<QS>(st + kStageP, wq + 2 * a, ks, lane);
-#pragma unroll
-      for (int a = 0; a < NM; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[b], fq[a], acc[a][b], 0, 0, 0);
-    }
-    lds_barrier();  // the stage may be refilled
-  }
-  // lane l holds Q row l % 32 of each block and, in elements 4q .. 4q + 3, the
-  // columns 8q + 4 (l / 32) + 0..3
-#pragma unroll
-  for (int a = 0; a < NM; ++a) {
-    const int m = (wq + 2 * a) * 32 + (lane & 31);
-    if (m >= t.rows) continue;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int c0 = (wp + 4 * b) * 32;
-      if (c0 >= t.cols) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v[4] = {acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-        store_tile<OP>(P, t, m, c0 + 8 * q + 4 * (lane >> 5), v);
+    bwd_stage<PS, QS, NM>(st, wq, wp, lane, acc, [&]() {
+      if constexpr (LOADER) {
+        if (kt + S - 1 < KT) issue(kt + S - 1, wr);
       }
+    });
+    rd = rd + 1 == S ? 0 : rd + 1;
+    wr = wr + 1 == S ? 0 : wr + 1;
+  }
+  lds_barrier();  // the ring is free
+  int dst[NM];
+  if constexpr (OP == BWD_DX) {
+#pragma unroll
+    for (int a = 0; a < NM; ++a) {
+      const int m = (wq + 2 * a) * 32 + (lane & 31);
+      dst[a] = m < t.rows ? P.row_dst[t.row0 + m] : 0;
     }
   }
+  if (wp * 64 < t.cols) {
+#pragma unroll
+    for (int a = 0; a < NM; ++a) {
+      const int m0 = (wq + 2 * a) * 32;
+      if (m0 < t.rows) store_block<OP>(P, t, lds + w * 8192, acc[a], m0, wp * 64, OP == BWD_DX ? dst[a] : 0, lane);
+    }
+  }
+  lds_barrier();  // ... for the next tile's loads
+}
+
+template <int OP, int QB>
+__device__ __forceinline__ void run_bwd_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
+  if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= 8 - kLoaders) bwd_tile_body<OP, QB, true>(P, t, lds);
+  else bwd_tile_body<OP, QB, false>(P, t, lds);
 }
 
 // Tile (p, n) of GU, DACT or DX: row band p, column tile n.
@@ -307,7 +439,7 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
 
 template <int OP>
 __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdParams P) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * (kStageP + kStageQ)];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kGemmLds];
   lds_t* lds = (lds_t*)smem;
   const int G = gridDim.x, b = blockIdx.x;
   const int lid = (G % 8 == 0) ? (b % 8) * (G / 8) + b / 8 : b;  // consecutive ids on one XCD
