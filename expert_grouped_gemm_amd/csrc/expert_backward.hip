@@ -43,7 +43,11 @@ constexpr int kBwdThreads = 512;             // 8 wavefronts: 2 (Q) x 4 (P)
 constexpr int kLoaders = 4;                  // the last 4 (one per SIMD) issue the ring's loads
 constexpr int kStageP = kTP * kBK * 2;       // bytes of the P operand in a stage
 
-// QB: 32-row blocks of the Q side of a tile (4 or 8).
+// QB: 32-row blocks of the Q side of a tile. A band of up to 256 rows takes
+// the smallest of 2, 4, 5, 6 and 8 that holds it: absent blocks cost no loads
+// and no MFMAs, and a smaller stage makes a deeper ring (4, 3, 3, 2 and 2
+// stages). Measured on the share (counts of 128 on the average, half of them
+// above): with 4 and 8 only, GU 501, DACT 267 and DX 542 us.
 __host__ __device__ constexpr int stage_q(int QB) { return QB * 32 * kBK * 2; }
 __host__ __device__ constexpr int bwd_ring(int QB) { return kGemmLds / (kStageP + stage_q(QB)); }
 
@@ -127,6 +131,8 @@ struct Loads {
     }
   }
 
+  // NT: with the non-temporal hint
+  template <bool NT>
   __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
     if constexpr (KS) {
       const int left = valid - kt * kBK;
@@ -135,7 +141,7 @@ struct Loads {
         const uint32_t off = (uint32_t)(2 * lw + (lane >> 5)) * pitch + lane_off;
 #pragma unroll
         for (int j = 0; j < NI; ++j)
-          __builtin_amdgcn_global_load_lds(b0 + (size_t)j * 8 * pitch + off, st + (4 * j + lw) * 1024, 16, 0, 0);
+          __builtin_amdgcn_global_load_lds(b0 + (size_t)j * 8 * pitch + off, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
       } else {
         // K row kk of the stage is row `rows` of lane kk: through idx (fetched
         // when the stage before was issued), or, in a last, partial stage,
@@ -147,7 +153,7 @@ struct Loads {
           const int r0 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw);
           const int r1 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw + 1);
           const uint8_t* g = base + (size_t)(lane < 32 ? r0 : r1) * pitch + lane_off;
-          __builtin_amdgcn_global_load_lds(g, st + (4 * j + lw) * 1024, 16, 0, 0);
+          __builtin_amdgcn_global_load_lds(g, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
         }
       }
     } else {
@@ -157,7 +163,7 @@ struct Loads {
         // columns that do not exist (a 128-wide tile) re-read the first ones
         const uint8_t* bj = direct ? b0 + (size_t)(j * 32 < valid ? j : j - NI / 2) * 32 * pitch : b0;
         const uint32_t off = direct ? lane_off : row_off[j] + lane_off;
-        __builtin_amdgcn_global_load_lds(bj + off, st + (4 * j + lw) * 1024, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(bj + off, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
       }
     }
   }
@@ -268,7 +274,7 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
   wave_lds_sync();
 }
 
-// One stage: MFMAs of a wavefront that owns Q blocks wq, wq + 2, ... and the
+// One stage: MFMAs of a wavefront that owns NM Q blocks wq, wq + 2, ... and the
 // two P blocks from 2 wp on. The fragments of step ks + 1 are read before the
 // MFMAs of step ks.
 template <bool PS, bool QS, int NM, class Issue>
@@ -297,15 +303,15 @@ __device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int l
 // One tile. A ring of bwd_ring(QB) stages in the LDS, one barrier per stage:
 // it shows the stage complete (each loader has waited for its own loads) and
 // every wavefront done with the slot the loaders refill next.
-template <int OP, int QB, bool LOADER>
+template <int OP, int QB, bool LOADER, int WQ, bool NT>
 __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile& t, lds_t* lds) {
   constexpr bool PS = p_strided(OP), QS = q_strided(OP);
-  constexpr int NM = QB / 2, NIQ = QS ? 8 : QB, LD = 8 + NIQ;
+  constexpr int NM = (QB + 1 - WQ) / 2, NIQ = QS ? 8 : QB, LD = 8 + NIQ;
   constexpr int S = bwd_ring(QB), SB = kStageP + stage_q(QB);
   static_assert(!QS || QB == 8, "a strided Q side has 256 columns");
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wq = w & 1, wp = w >> 1, lw = w - 4;
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w >> 1, lw = w - 4;
   f32x16 acc[NM][2];
 #pragma unroll
   for (int a = 0; a < NM; ++a)
@@ -318,8 +324,8 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
   Loads<PS, 8> lp;
   Loads<QS, NIQ> lq;
   auto issue = [&](int kt, int slot) {
-    lp.issue(kt, lds + slot * SB, lw, lane);
-    lq.issue(kt, lds + slot * SB + kStageP, lw, lane);
+    lp.template issue<NT>(kt, lds + slot * SB, lw, lane);
+    lq.template issue<false>(kt, lds + slot * SB + kStageP, lw, lane);
   };
   if constexpr (LOADER) {
     lp.init(t.P, lw, lane, true);
@@ -331,7 +337,10 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
   int rd = 0, wr = S - 1;
   for (int kt = 0; kt < KT; ++kt) {
     if constexpr (LOADER) {
-      if (S > 2 && kt + 1 < KT) wait_vmcnt<(S - 2) * LD>();
+      // the stages after kt that are in flight: S - 2, near the end fewer
+      const int after = KT - 1 - kt;
+      if (after >= S - 2) wait_vmcnt<(S - 2) * LD>();
+      else if (S > 3 && after == 1) wait_vmcnt<LD>();
       else wait_vmcnt<0>();
     }
     lds_barrier();
@@ -347,7 +356,7 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
         lds_barrier();
       }
     }
-    bwd_stage<PS, QS, NM>(st, wq, wp, lane, acc, [&]() {
+    bwd_stage<PS, QS, NM>(st, WQ, wp, lane, acc, [&]() {
       if constexpr (LOADER) {
         if (kt + S - 1 < KT) issue(kt + S - 1, wr);
       }
@@ -360,24 +369,40 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
   if constexpr (OP == BWD_DX) {
 #pragma unroll
     for (int a = 0; a < NM; ++a) {
-      const int m = (wq + 2 * a) * 32 + (lane & 31);
+      const int m = (WQ + 2 * a) * 32 + (lane & 31);
       dst[a] = m < t.rows ? P.row_dst[t.row0 + m] : 0;
     }
   }
   if (wp * 64 < t.cols) {
 #pragma unroll
     for (int a = 0; a < NM; ++a) {
-      const int m0 = (wq + 2 * a) * 32;
+      const int m0 = (WQ + 2 * a) * 32;
       if (m0 < t.rows) store_block<OP>(P, t, lds + w * 8192, acc[a], m0, wp * 64, OP == BWD_DX ? dst[a] : 0, lane);
     }
   }
   lds_barrier();  // ... for the next tile's loads
 }
 
-template <int OP, int QB>
+// A wavefront's role: loader or not, and its row of the 2 x 4 wavefront grid.
+template <int OP, int QB, bool NT>
 __device__ __forceinline__ void run_bwd_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
-  if (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) >= 8 - kLoaders) bwd_tile_body<OP, QB, true>(P, t, lds);
-  else bwd_tile_body<OP, QB, false>(P, t, lds);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (w >= 8 - kLoaders) {
+    if (w & 1) bwd_tile_body<OP, QB, true, 1, NT>(P, t, lds);
+    else bwd_tile_body<OP, QB, true, 0, NT>(P, t, lds);
+  } else {
+    if (w & 1) bwd_tile_body<OP, QB, false, 1, NT>(P, t, lds);
+    else bwd_tile_body<OP, QB, false, 0, NT>(P, t, lds);
+  }
+}
+
+template <int OP, bool NT>
+__device__ __forceinline__ void run_band_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
+  if (t.rows <= 64) run_bwd_tile<OP, 2, NT>(P, t, lds);
+  else if (t.rows <= 128) run_bwd_tile<OP, 4, NT>(P, t, lds);
+  else if (t.rows <= 160) run_bwd_tile<OP, 5, NT>(P, t, lds);
+  else if (t.rows <= 192) run_bwd_tile<OP, 6, NT>(P, t, lds);
+  else run_bwd_tile<OP, 8, NT>(P, t, lds);
 }
 
 // Tile (p, n) of GU, DACT or DX: row band p, column tile n.
@@ -453,8 +478,10 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
       int p, n;
       raster(i, nb, N, P.group_m, p, n);
       const BwdTile t = band_tile<OP>(P, p, n);
-      if (t.rows <= 128) run_bwd_tile<OP, 4>(P, t, lds);
-      else run_bwd_tile<OP, 8>(P, t, lds);
+      // weights of an expert with one band are read once per launch (see
+      // streams_once)
+      if (P.band_expert[p] & kBandSingle) run_band_tile<OP, true>(P, t, lds);
+      else run_band_tile<OP, false>(P, t, lds);
     }
   } else {
     const int M = ((OP == BWD_DW2 ? P.d : 2 * P.f) + kBM - 1) / kBM;
@@ -463,7 +490,7 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
       const int e = (int)(i / (M * N));
       int m, n;
       raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
-      run_bwd_tile<OP, 8>(P, weight_tile<OP>(P, e, m, n), lds);
+      run_bwd_tile<OP, 8, false>(P, weight_tile<OP>(P, e, m, n), lds);
     }
   }
 }
