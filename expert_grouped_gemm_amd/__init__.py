@@ -198,42 +198,37 @@ def _check(status: int, where: str):
 def _operand(where: str, name: str, t, dtype, numel: int, optional: bool = False) -> Optional[int]:
     """The address of a call's tensor, once its type and size are the ones the
     library will assume (the C ABI sees only a pointer)."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{where}: {name} is missing")
-    ptr = _ptr(t)
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{where}: {name} is missing" if t is None else f"{where}: {name} is not a tensor")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous and on the GPU")
+    if t.dtype is not dtype:
         raise ValueError(f"{where}: {name} is {t.dtype}, expected {dtype}")
     if t.numel() < numel:
         raise ValueError(f"{where}: {name} holds {t.numel()} elements, needs {numel}")
-    return ptr
+    return t.data_ptr()
 
 
-class _On:
-    """The device of a call's tensors made current, for the launch (a kernel
-    runs on the device that is current): every tensor has to be on it, and a
-    given stream has to be one of its streams."""
-
-    def __init__(self, where: str, stream, *tensors):
-        devs = {t.device for t in tensors if isinstance(t, torch.Tensor) and t.device.type == "cuda"}
-        if len(devs) > 1:
-            raise ValueError(f"{where}: tensors on several devices {sorted(map(str, devs))}")
-        self.dev = next(iter(devs), None)
-        if self.dev is not None and getattr(stream, "device", self.dev) != self.dev:
-            raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {self.dev}")
-        self.stream = stream
-        self.guard = None
-
-    def __enter__(self) -> int:
-        if self.dev is not None and self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _launch(where: str, stream, tensors, call):
+    """call(stream address) with the device of the call's tensors current (a
+    kernel runs on the device that is current): every tensor has to be on it,
+    and a given stream has to be one of its streams."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on cuda:{dev} and cuda:{t.get_device()}")
+    on = getattr(stream, "device", None)
+    if on is not None and on.index != dev:
+        raise ValueError(f"{where}: the stream is on {on}, the tensors on cuda:{dev}")
+    if dev == torch.cuda.current_device():
+        status = call(_stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = call(_stream(stream))
+    if status != 0:
+        raise MoEError(status, "moe_" + where)
 
 
 def workspace_size(p: Problem) -> int:
@@ -402,8 +397,8 @@ def combine_backward(p: Problem, dY, combine_buf, tok_off, topk_idx, topk_w, d_c
             _operand(w, "d_combine_buf", d_combine_buf, torch.bfloat16, cap * p.d),
             _operand(w, "d_topk_w", d_topk_w, torch.float32, p.T * p.k),
             _operand(w, "d_logits", d_logits, torch.float32, p.T * p.E_global, optional=True))
-    with _On(w, stream, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf, d_topk_w, d_logits) as s:
-        _check(lib().moe_combine_backward(ctypes.byref(p), *args, s), "moe_combine_backward")
+    _launch(w, stream, (dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf, d_topk_w, d_logits),
+            lambda s: lib().moe_combine_backward(ctypes.byref(p), *args, s))
 
 
 def backward_workspace_size(p: Problem) -> int:
@@ -431,8 +426,8 @@ def expert_backward(p: Problem, X, row_src, offsets, row_dst, W1, W2, d_combine_
             _operand(w, "d_combine_buf", d_combine_buf, bf, cap * p.d),
             _operand(w, "d_x_slots", d_x_slots, bf, cap * p.d), _operand(w, "dW1", dW1, bf, El * 2 * p.f * p.d),
             _operand(w, "dW2", dW2, bf, El * p.d * p.f), _operand(w, "workspace", workspace, torch.uint8, 0))
-    with _On(w, stream, X, row_src, offsets, row_dst, W1, W2, d_combine_buf, d_x_slots, dW1, dW2, workspace) as s:
-        _check(lib().moe_expert_backward(ctypes.byref(p), *args, workspace.numel(), s), "moe_expert_backward")
+    _launch(w, stream, (X, row_src, offsets, row_dst, W1, W2, d_combine_buf, d_x_slots, dW1, dW2, workspace),
+            lambda s: lib().moe_expert_backward(ctypes.byref(p), *args, workspace.numel(), s))
 
 
 def dispatch_backward(p: Problem, d_x_slots, tok_off, dX, dX_fp32=None, stream=None):
@@ -442,17 +437,20 @@ def dispatch_backward(p: Problem, d_x_slots, tok_off, dX, dX_fp32=None, stream=N
             _operand(w, "tok_off", tok_off, torch.int32, p.T + 1),
             _operand(w, "dX", dX, torch.bfloat16, p.T * p.d),
             _operand(w, "dX_fp32", dX_fp32, torch.float32, p.T * p.d, optional=True))
-    with _On(w, stream, d_x_slots, tok_off, dX, dX_fp32) as s:
-        _check(lib().moe_dispatch_backward(ctypes.byref(p), *args, s), "moe_dispatch_backward")
+    _launch(w, stream, (d_x_slots, tok_off, dX, dX_fp32),
+            lambda s: lib().moe_dispatch_backward(ctypes.byref(p), *args, s))
 
 
-def _mxfp4_shape(where: str, x):
+def _mxfp4_rows(where: str, name: str, x):
+    """Rows, columns and whether fp32, of the values' tensor of a codec call."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
-        raise ValueError(f"{where}: expected a tensor of rows")
+        raise ValueError(f"{where}: {name} must be a tensor of rows")
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        raise ValueError(f"{where}: {name} is {x.dtype}, expected torch.bfloat16 or torch.float32")
     cols = x.shape[-1]
     if cols < 1 or cols % 32:
         raise ValueError(f"{where}: rows of {cols} elements are not whole blocks of 32")
-    return x.numel() // cols, cols
+    return x.numel() // cols, cols, int(x.dtype is torch.float32)
 
 
 def mxfp4_quantize(x, codes, scales, stream=None):
@@ -460,24 +458,22 @@ def mxfp4_quantize(x, codes, scales, stream=None):
     [..., cols/2] and E8M0 scales uint8 [..., cols/32], blocks along the last
     dimension."""
     w = "mxfp4_quantize"
-    rows, cols = _mxfp4_shape(w, x)
+    rows, cols, f32 = _mxfp4_rows(w, "x", x)
     n = rows * cols
-    args = (_operand(w, "x", x, (torch.bfloat16, torch.float32), n), int(x.dtype == torch.float32), rows, cols,
-            _operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32))
-    with _On(w, stream, x, codes, scales) as s:
-        _check(lib().moe_mxfp4_quantize(*args, s), "moe_mxfp4_quantize")
+    px, pc, ps = (_operand(w, "x", x, x.dtype, n), _operand(w, "codes", codes, torch.uint8, n // 2),
+                  _operand(w, "scales", scales, torch.uint8, n // 32))
+    _launch(w, stream, (x, codes, scales), lambda s: lib().moe_mxfp4_quantize(px, f32, rows, cols, pc, ps, s))
 
 
 def mxfp4_dequantize(codes, scales, out, stream=None):
     """moe_mxfp4_dequantize: the values of MXFP4 codes and scales into out
     [..., cols] (bf16 or fp32)."""
     w = "mxfp4_dequantize"
-    rows, cols = _mxfp4_shape(w, out)
+    rows, cols, f32 = _mxfp4_rows(w, "out", out)
     n = rows * cols
-    args = (_operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32),
-            rows, cols, _operand(w, "out", out, (torch.bfloat16, torch.float32), n), int(out.dtype == torch.float32))
-    with _On(w, stream, codes, scales, out) as s:
-        _check(lib().moe_mxfp4_dequantize(*args, s), "moe_mxfp4_dequantize")
+    pc, ps, po = (_operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32),
+                  _operand(w, "out", out, out.dtype, n))
+    _launch(w, stream, (codes, scales, out), lambda s: lib().moe_mxfp4_dequantize(pc, ps, rows, cols, po, f32, s))
 
 
 def mxfp4_linear1(p: Problem, X, X_scale, row_src, offsets, W1, W1_scale, H, workspace, stream=None):
@@ -491,8 +487,8 @@ def mxfp4_linear1(p: Problem, X, X_scale, row_src, offsets, W1, W1_scale, H, wor
             _operand(w, "offsets", offsets, torch.int32, El + 1),
             _operand(w, "W1", W1, u8, El * p.f * p.d), _operand(w, "W1_scale", W1_scale, u8, El * p.f * p.d // 16),
             _operand(w, "H", H, torch.bfloat16, cap * p.f), _operand(w, "workspace", workspace, u8, 0))
-    with _On(w, stream, X, X_scale, row_src, offsets, W1, W1_scale, H, workspace) as s:
-        _check(lib().moe_mxfp4_linear1(ctypes.byref(p), *args, workspace.numel(), s), "moe_mxfp4_linear1")
+    _launch(w, stream, (X, X_scale, row_src, offsets, W1, W1_scale, H, workspace),
+            lambda s: lib().moe_mxfp4_linear1(ctypes.byref(p), *args, workspace.numel(), s))
 
 
 def mxfp4_linear2(p: Problem, H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace, stream=None):
@@ -504,8 +500,8 @@ def mxfp4_linear2(p: Problem, H, H_scale, offsets, row_dst, W2, W2_scale, combin
             _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
             _operand(w, "W2", W2, u8, El * p.f * p.d // 2), _operand(w, "W2_scale", W2_scale, u8, El * p.f * p.d // 32),
             _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d), _operand(w, "workspace", workspace, u8, 0))
-    with _On(w, stream, H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace) as s:
-        _check(lib().moe_mxfp4_linear2(ctypes.byref(p), *args, workspace.numel(), s), "moe_mxfp4_linear2")
+    _launch(w, stream, (H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace),
+            lambda s: lib().moe_mxfp4_linear2(ctypes.byref(p), *args, workspace.numel(), s))
 
 
 def check_workspace(p: Problem, workspace, stream=None):

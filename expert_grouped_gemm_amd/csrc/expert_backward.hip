@@ -194,6 +194,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 struct BwdTile {
   Side P, Q;
   int ktiles;
+  int krot;     // stage kt holds K slice (kt + krot) mod ktiles
   int e;        // expert
   int row0;     // first row (GU, DACT, DX: of the band; DW: first output row)
   int rows;     // valid Q rows / output rows
@@ -268,7 +269,14 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
       const int r = j * 8 + (lane >> 3);
       const i32x4 v = *(const lds_i32x4*)(wl + r * 128 + ((c ^ (r & 7)) << 4));
       const size_t row = OP == BWD_DX ? (size_t)__shfl(dst, r, 64) : (size_t)t.row0 + m0 + r;
-      if (m0 + r < t.rows) *reinterpret_cast<i32x4*>(out + row * ld + t.col0 + c0 + c * 8) = v;
+      i32x4* at = reinterpret_cast<i32x4*>(out + row * ld + t.col0 + c0 + c * 8);
+      // the weight gradients are not read again here: past the caches. (DX's
+      // rows are, by the dispatch's gradient.) Measured: DW1 of the share 832
+      // -> 768 us, of 16384 rows 4640 -> 4300; DX with the hint 3% slower.
+      if (m0 + r < t.rows) {
+        if constexpr (OP == BWD_DX) *at = v;
+        else __builtin_nontemporal_store(v, at);
+      }
     }
   }
   wave_lds_sync();
@@ -323,7 +331,9 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
   const int KT = t.ktiles;
   Loads<PS, 8> lp;
   Loads<QS, NIQ> lq;
-  auto issue = [&](int kt, int slot) {
+  auto issue = [&](int stage, int slot) {
+    int kt = stage;
+    if constexpr (!QS) kt = stage + t.krot >= KT ? stage + t.krot - KT : stage + t.krot;
     lp.template issue<NT>(kt, lds + slot * SB, lw, lane);
     lq.template issue<false>(kt, lds + slot * SB + kStageP, lw, lane);
   };
@@ -410,6 +420,10 @@ template <int OP>
 __device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n) {
   BwdTile t;
   t.e = P.band_expert[p] & kBandExpertMask;
+  // bands of different experts run together: DACT starts their K slices apart,
+  // or all of them stream the same HBM channels (see kKRot; the share's DACT
+  // 266 -> 251 us, nothing to gain for GU and DX)
+  const bool once = (P.band_expert[p] & kBandSingle) != 0;
   t.row0 = P.band_row0[p];
   t.rows = P.band_rows[p];
   t.col0 = n * kTP;
@@ -419,17 +433,20 @@ __device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n) {
   if constexpr (OP == BWD_GU) {
     t.cols = min(kTP, 2 * P.f - t.col0);
     t.ktiles = P.d / kBK;
+    t.krot = 0;
     t.P = Side{w1 + (size_t)t.col0 * db, db, t.cols, 0, nullptr, 1};
     t.Q = P.row_src ? Side{P.X, db, t.rows, 0, P.row_src + t.row0, P.k}
                     : Side{P.X + (size_t)t.row0 * db, db, t.rows, 0, nullptr, 1};
   } else if constexpr (OP == BWD_DACT) {
     t.cols = min(kTP, P.f - t.col0);
     t.ktiles = P.d / kBK;
+    t.krot = once ? t.e * kKRot % t.ktiles : 0;
     t.P = Side{w2 + (size_t)t.col0 * 2, fb, P.d, t.cols / 8, nullptr, 1};
     t.Q = Side{P.dO, db, t.rows, 0, P.row_dst + t.row0, 1};
   } else {
     t.cols = min(kTP, P.d - t.col0);
     t.ktiles = 2 * P.f / kBK;
+    t.krot = 0;
     t.P = Side{w1 + (size_t)t.col0 * 2, db, 2 * P.f, t.cols / 8, nullptr, 1};
     t.Q = Side{reinterpret_cast<const uint8_t*>(P.dH) + (size_t)t.row0 * (2 * fb), 2 * fb, t.rows, 0, nullptr, 1};
   }
