@@ -211,6 +211,12 @@ def _operand(where: str, name: str, t, dtype, numel: int, optional: bool = False
     return t.data_ptr()
 
 
+# The current stream's address: torch's raw accessor where it has one (0.2 us;
+# building the Stream object takes 2.8, a third of a small call).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch(where: str, stream, tensors, call):
     """call(stream address) with the device of the call's tensors current (a
     kernel runs on the device that is current): every tensor has to be on it,
@@ -223,7 +229,7 @@ def _launch(where: str, stream, tensors, call):
     if on is not None and on.index != dev:
         raise ValueError(f"{where}: the stream is on {on}, the tensors on cuda:{dev}")
     if dev == torch.cuda.current_device():
-        status = call(_stream(stream))
+        status = call(_current_stream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
             status = call(_stream(stream))

@@ -38,18 +38,21 @@ __host__ __device__ constexpr bool p_strided(int OP) { return OP != BWD_GU; }
 __host__ __device__ constexpr bool q_strided(int OP) { return OP >= BWD_DW2; }
 
 constexpr int kBK = 64;                      // K values per stage
-constexpr int kTP = 256;                     // columns (P side) of a tile
 constexpr int kBwdThreads = 512;             // 8 wavefronts: 2 (Q) x 4 (P)
 constexpr int kLoaders = 4;                  // the last 4 (one per SIMD) issue the ring's loads
-constexpr int kStageP = kTP * kBK * 2;       // bytes of the P operand in a stage
 
-// QB: 32-row blocks of the Q side of a tile. A band of up to 256 rows takes
-// the smallest of 2, 4, 5, 6 and 8 that holds it: absent blocks cost no loads
-// and no MFMAs, and a smaller stage makes a deeper ring (4, 3, 3, 2 and 2
-// stages). Measured on the share (counts of 128 on the average, half of them
-// above): with 4 and 8 only, GU 501, DACT 267 and DX 542 us.
-__host__ __device__ constexpr int stage_q(int QB) { return QB * 32 * kBK * 2; }
-__host__ __device__ constexpr int bwd_ring(int QB) { return kGemmLds / (kStageP + stage_q(QB)); }
+// A tile has PB 32-column blocks (8, or 4 in the last, partly idle round of the
+// persistent grid: twice as many tiles of half the width) and QB 32-row blocks.
+// A band of up to 256 rows takes the smallest of 2, 4, 5, 6 and 8 that holds
+// it: absent blocks cost no loads and no MFMAs, and a smaller stage makes a
+// deeper ring. Measured on the share (counts of 128 on the average, half of them
+// above): with 4 and 8 only, GU 501, DACT 267 and DX 542 us; with all, 409, 266
+// and 515.
+__host__ __device__ constexpr int stage_bytes_of(int blocks) { return blocks * 32 * kBK * 2; }
+__host__ __device__ constexpr int bwd_ring(int PB, int QB) {
+  const int s = kGemmLds / stage_bytes_of(PB + QB);
+  return s > 6 ? 6 : s;
+}
 
 struct BwdParams {
   const uint8_t* X;          // token rows [T, d] (through row_src) or expert-ordered rows
@@ -91,103 +94,123 @@ __device__ __forceinline__ int ks_swizzle(int kk) { return (kk & 3) << 2; }
 
 // The ring's loads of one side, as one loader wavefront issues them: NI
 // instructions of 1 KiB per stage. An instruction takes 8 rows of 128 bytes
-// (KC) or 2 K rows of 512 (KS); loader lw of 4 takes instructions 4 j + lw, so
-// its lanes' rows advance by a uniform step from one to the next (and the
-// swizzle, which depends on the row modulo 16 or 4, not at all): the address is
-// a uniform base plus one 32-bit lane offset.
-template <bool KS, int NI>
-struct Loads {
+// (KC), 2 K rows of 512 bytes or 4 of 256 (KS); loader lw of 4 takes
+// instructions 4 j + lw, so its lanes' rows advance by a uniform step from one
+// to the next, and the swizzle, which depends on the row modulo 16 or 4, stays:
+// an address is a uniform base plus one 32-bit lane offset.
+
+// A weight matrix: every row exists, at its own place. Of a 256-column tile
+// only 128 columns may exist: the others re-read those. NT: with the
+// non-temporal hint.
+template <bool KS, int BLOCKS, bool NT>
+struct WeightLoads {
+  static constexpr int NI = BLOCKS;                       // BLOCKS * 4 KiB over 4 loaders
+  static constexpr int CPR = KS ? BLOCKS * 4 : 8;         // 16-byte chunks per LDS row
+  static constexpr int RPI = 64 / CPR;                    // rows per instruction
+  const uint8_t* base;
+  uint32_t pitch, lane_off;
+  int valid;
+
+  __device__ __forceinline__ void init(const Side& s, int lw, int lane) {
+    base = s.base;
+    pitch = s.pitch;
+    valid = s.valid;
+    const int r = lw * RPI + lane / CPR, c = lane % CPR;
+    if constexpr (KS) lane_off = r * pitch + (((c ^ ks_swizzle(r)) & (s.chunks - 1)) << 4);
+    else lane_off = r * pitch + ((c ^ chunk_swizzle<128>(r)) << 4);
+  }
+  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int) {
+    const uint8_t* b0 = base + (KS ? (size_t)kt * kBK * pitch : (size_t)kt * (kBK * 2));
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int step = KS || j * 4 * RPI < valid ? j : j - NI / 2;
+      __builtin_amdgcn_global_load_lds(b0 + (size_t)step * (4 * RPI) * pitch + lane_off, st + (4 * j + lw) * 1024, 16, 0,
+                                       NT ? kCpolNT : 0);
+    }
+  }
+};
+
+// Rows of a band (KC), perhaps through idx, the last one repeated.
+template <int BLOCKS>
+struct BandLoads {
+  static constexpr int NI = BLOCKS;
+  const uint8_t* base;
+  uint32_t off[NI];
+
+  __device__ __forceinline__ void init(const Side& s, int lw, int lane) {
+    base = s.base;
+    const int r = lw * 8 + (lane >> 3);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int row = min(j * 32 + r, s.valid - 1);
+      off[j] = (uint32_t)(s.idx ? s.idx[row] / s.div : row) * s.pitch + (((lane & 7) ^ chunk_swizzle<128>(r)) << 4);
+    }
+  }
+  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int) {
+    const uint8_t* b0 = base + (size_t)kt * (kBK * 2);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) __builtin_amdgcn_global_load_lds(b0 + off[j], st + (4 * j + lw) * 1024, 16, 0, 0);
+  }
+};
+
+// An expert's rows as K (KS, 256 columns), perhaps through idx. Lane kk looks
+// up K row kk of a stage for all lanes; rows past the last re-read it (the
+// stage's LDS rows are zeroed). The first two stages' rows are kept while the
+// expert stays, so that the next tile's first loads wait for no index; later
+// stages' are fetched when the stage before is issued.
+struct RowLoads {
+  static constexpr int NI = 8;
   const uint8_t* base;
   uint32_t pitch, lane_off;
   const int32_t* idx;
-  int div, valid;
-  uint32_t row_off[KS ? 1 : NI];  // KC with rows of their own places
-  bool direct;
-  int next;                       // KS through idx: this lane's K row of the next stage to issue
+  int div, valid, r0, r1, next;
 
-  __device__ __forceinline__ void init(const Side& s, int lw, int lane, bool plain_rows) {
+  __device__ __forceinline__ int look_up(int kt, int lane) const {
+    const int row = min(kt * kBK + lane, valid - 1);
+    return idx ? idx[row] / div : row;
+  }
+  __device__ __forceinline__ void init(const Side& s, int lw, int lane, bool same_expert) {
     base = s.base;
     pitch = s.pitch;
     idx = s.idx;
     div = s.div;
     valid = s.valid;
-    direct = plain_rows;
-    if constexpr (KS) {
-      const int kk = 2 * lw + (lane >> 5);
-      lane_off = (((lane & 31) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
-      direct = idx == nullptr;
-      next = idx && valid > 0 ? idx[min(lane, valid - 1)] / div : 0;
-    } else {
-      const int r = lw * 8 + (lane >> 3);
-      const uint32_t chunk = ((lane & 7) ^ chunk_swizzle<128>(r)) << 4;
-      lane_off = direct ? r * pitch + chunk : chunk;
-      if (!direct) {
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          const int row = min(j * 32 + r, valid - 1);
-          row_off[j] = (uint32_t)(idx ? idx[row] / div : row) * pitch;
-        }
-      }
+    const int kk = 2 * lw + (lane >> 5);
+    lane_off = (((lane & 31) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
+    if (!same_expert && valid > 0) {
+      r0 = look_up(0, lane);
+      r1 = look_up(1, lane);
     }
   }
-
-  // NT: with the non-temporal hint
-  template <bool NT>
   __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
-    if constexpr (KS) {
-      const int left = valid - kt * kBK;
-      if (direct && left >= kBK) {
-        const uint8_t* b0 = base + (size_t)kt * kBK * pitch;
-        const uint32_t off = (uint32_t)(2 * lw + (lane >> 5)) * pitch + lane_off;
+    const int rows = kt == 0 ? r0 : kt == 1 ? r1 : next;
+    if (kt > 0 && (kt + 1) * kBK < valid) next = look_up(kt + 1, lane);
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
-          __builtin_amdgcn_global_load_lds(b0 + (size_t)j * 8 * pitch + off, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
-      } else {
-        // K row kk of the stage is row `rows` of lane kk: through idx (fetched
-        // when the stage before was issued), or, in a last, partial stage,
-        // rows past the end re-reading the last (they are zeroed in the LDS)
-        const int rows = direct ? kt * kBK + min(lane, left - 1) : next;
-        if (!direct) next = idx[min((kt + 1) * kBK + lane, valid - 1)] / div;
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          const int r0 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw);
-          const int r1 = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw + 1);
-          const uint8_t* g = base + (size_t)(lane < 32 ? r0 : r1) * pitch + lane_off;
-          __builtin_amdgcn_global_load_lds(g, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
-        }
-      }
-    } else {
-      const uint8_t* b0 = base + (size_t)kt * 128;
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        // columns that do not exist (a 128-wide tile) re-read the first ones
-        const uint8_t* bj = direct ? b0 + (size_t)(j * 32 < valid ? j : j - NI / 2) * 32 * pitch : b0;
-        const uint32_t off = direct ? lane_off : row_off[j] + lane_off;
-        __builtin_amdgcn_global_load_lds(bj + off, st + (4 * j + lw) * 1024, 16, 0, NT ? kCpolNT : 0);
-      }
+    for (int j = 0; j < NI; ++j) {
+      const int a = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw);
+      const int b = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw + 1);
+      __builtin_amdgcn_global_load_lds(base + (size_t)(lane < 32 ? a : b) * pitch + lane_off, st + (4 * j + lw) * 1024,
+                                       16, 0, 0);
     }
   }
 };
 
 // Fragment of the 16 K values of step ks and the 32 rows / columns of block
-// blk: lane l holds row blk * 32 + l % 32, K values 8 (l / 32) .. + 7.
-template <bool KS>
+// blk: lane l holds row blk * 32 + l % 32, K values 8 (l / 32) .. + 7. BLOCKS:
+// the side's blocks (KS: its LDS rows hold 64 bytes of each).
+template <bool KS, int BLOCKS>
 __device__ __forceinline__ bf16x8 fragment(const lds_t* st, int blk, int ks, int lane) {
   const int hi = lane >> 5;
   if constexpr (KS) {
     const int kk = ks * 16 + hi * 8 + ((lane & 15) >> 2);
     const int col = blk * 32 + (lane & 16) + (lane & 3) * 4;
-    const lds_t* a = st + kk * 512 + (((col >> 3) ^ ks_swizzle(kk)) << 4) + (col & 4) * 2;
+    const lds_t* a = st + kk * (BLOCKS * 64) + (((col >> 3) ^ ks_swizzle(kk)) << 4) + (col & 4) * 2;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
-    const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * 512));
+    const s16x4 up = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * BLOCKS * 64));
     return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]});
   } else {
     return *(const lds_bf16x8*)(st + lds_off<128>(blk * 32 + (lane & 31), ks * 2 + hi));
   }
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)f32_to_bf16_rne(a) | ((uint32_t)f32_to_bf16_rne(b) << 16);
 }
 
 // A tile: where its operands are and where its results go.
@@ -202,30 +225,30 @@ struct BwdTile {
   int cols;     // valid output columns (128 or 256)
 };
 
-// The results of one 32-row block of a wavefront (its 64 columns), through the
-// wavefront's own 8 KiB of the free ring: a lane of the accumulator holds 4
-// consecutive columns of a row, whose direct store would write 8 or 16 bytes
-// into each of 32 rows; read back, every store writes whole 128-byte lines of
-// few rows. m0: the block's first row; dst: this lane's output row of block
-// row lane % 32 (DX: its slot).
-template <int OP>
-__device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t, lds_t* wl, const f32x16 (&acc)[2],
+// The results of one 32-row block of a wavefront (its NB * 32 columns), through
+// the wavefront's own LDS: a lane of the accumulator holds 4 consecutive columns
+// of a row, whose direct store would write 8 or 16 bytes into each of 32 rows;
+// read back, every store writes whole 128-byte lines of few rows (64 bytes with
+// NB = 1). m0: the block's first row; dst: this lane's output row of block row
+// lane % 32 (DX: its slot).
+template <int OP, int NB>
+__device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t, lds_t* wl, const f32x16 (&acc)[NB],
                                             int m0, int c0, int dst, int lane) {
   const int lr = lane & 31, hi = lane >> 5;
   if constexpr (OP == BWD_GU || OP == BWD_DACT) {
-    // 32 rows of 256 bytes (fp32), 16-byte chunks swizzled by row
+    constexpr int C = 8 * NB;  // 16-byte chunks of a row (fp32), swizzled by row
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *(lds_f32x4*)(wl + lr * 256 + (((b * 8 + 2 * q + hi) ^ (lr & 15)) << 4)) =
+        *(lds_f32x4*)(wl + lr * (C * 16) + (((b * 8 + 2 * q + hi) ^ (lr & (C - 1))) << 4)) =
             f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
     wave_lds_sync();
-    const int c = lane & 15;
+    const int c = lane & (C - 1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = j * 4 + (lane >> 4);
-      const f32x4 v = *(const lds_f32x4*)(wl + r * 256 + ((c ^ (r & 15)) << 4));
+    for (int j = 0; j < C / 2; ++j) {
+      const int r = j * (64 / C) + lane / C;
+      const f32x4 v = *(const lds_f32x4*)(wl + r * (C * 16) + ((c ^ (r & (C - 1))) << 4));
       if (m0 + r >= t.rows) continue;
       const size_t row = (size_t)t.row0 + m0 + r;
       const int col = t.col0 + c0 + c * 4;
@@ -244,30 +267,30 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
           du[i] = v[i] * gs;
           dg[i] = v[i] * u[i] * (s + gs * (1.0f - s));
         }
-        *reinterpret_cast<uint2*>(P.act + row * P.f + col) = make_uint2(pack2(a[0], a[1]), pack2(a[2], a[3]));
+        *reinterpret_cast<uint2*>(P.act + row * P.f + col) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
         uint16_t* dh = P.dH + row * (2 * (size_t)P.f) + col;
-        *reinterpret_cast<uint2*>(dh) = make_uint2(pack2(dg[0], dg[1]), pack2(dg[2], dg[3]));
-        *reinterpret_cast<uint2*>(dh + P.f) = make_uint2(pack2(du[0], du[1]), pack2(du[2], du[3]));
+        *reinterpret_cast<uint2*>(dh) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
+        *reinterpret_cast<uint2*>(dh + P.f) = make_uint2(pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3]));
       }
     }
   } else {
-    // 32 rows of 128 bytes (bf16)
+    constexpr int C = 4 * NB;  // 16-byte chunks of a row (bf16)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        *(lds_u32x2*)(wl + lr * 128 + (((b * 4 + q) ^ (lr & 7)) << 4) + hi * 8) =
-            u32x2{pack2(acc[b][4 * q], acc[b][4 * q + 1]), pack2(acc[b][4 * q + 2], acc[b][4 * q + 3])};
+        *(lds_u32x2*)(wl + lr * (C * 16) + (((b * 4 + q) ^ (lr & (C - 1))) << 4) + hi * 8) =
+            u32x2{pack_bf16(acc[b][4 * q], acc[b][4 * q + 1]), pack_bf16(acc[b][4 * q + 2], acc[b][4 * q + 3])};
     wave_lds_sync();
-    const int c = lane & 7;
+    const int c = lane & (C - 1);
     const size_t ld = OP == BWD_DW2 ? P.f : P.d;
     uint16_t* out = OP == BWD_DX    ? P.dxs
                     : OP == BWD_DW2 ? P.dW2 + (size_t)t.e * P.d * P.f
                                     : P.dW1 + (size_t)t.e * 2 * P.f * P.d;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = j * 8 + (lane >> 3);
-      const i32x4 v = *(const lds_i32x4*)(wl + r * 128 + ((c ^ (r & 7)) << 4));
+    for (int j = 0; j < C / 2; ++j) {
+      const int r = j * (64 / C) + lane / C;
+      const i32x4 v = *(const lds_i32x4*)(wl + r * (C * 16) + ((c ^ (r & (C - 1))) << 4));
       const size_t row = OP == BWD_DX ? (size_t)__shfl(dst, r, 64) : (size_t)t.row0 + m0 + r;
       i32x4* at = reinterpret_cast<i32x4*>(out + row * ld + t.col0 + c0 + c * 8);
       // the weight gradients are not read again here: past the caches. (DX's
@@ -283,17 +306,18 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
 }
 
 // One stage: MFMAs of a wavefront that owns NM Q blocks wq, wq + 2, ... and the
-// two P blocks from 2 wp on. The fragments of step ks + 1 are read before the
-// MFMAs of step ks.
-template <bool PS, bool QS, int NM, class Issue>
-__device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int lane, f32x16 (&acc)[NM][2],
+// P blocks from wp * PB / 4 on. The fragments of step ks + 1 are read before
+// the MFMAs of step ks; issue() issues the loader's loads behind the first.
+template <bool PS, bool QS, int PB, int QB, int NM, class Issue>
+__device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int lane, f32x16 (&acc)[NM][PB / 4],
                                           const Issue& issue) {
-  bf16x8 fp[2][2], fq[2][NM];
+  constexpr int NB = PB / 4;
+  bf16x8 fp[2][NB], fq[2][NM];
   auto read = [&](int ks, int buf) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) fp[buf][b] = fragment<PS>(st, 2 * wp + b, ks, lane);
+    for (int b = 0; b < NB; ++b) fp[buf][b] = fragment<PS, PB>(st, NB * wp + b, ks, lane);
 #pragma unroll
-    for (int a = 0; a < NM; ++a) fq[buf][a] = fragment<QS>(st + kStageP, wq + 2 * a, ks, lane);
+    for (int a = 0; a < NM; ++a) fq[buf][a] = fragment<QS, QB>(st + stage_bytes_of(PB), wq + 2 * a, ks, lane);
   };
   read(0, 0);
 #pragma unroll
@@ -303,70 +327,64 @@ __device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int l
 #pragma unroll
     for (int a = 0; a < NM; ++a)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < NB; ++b)
         acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fp[ks & 1][b], fq[ks & 1][a], acc[a][b], 0, 0, 0);
   }
 }
 
-// One tile. A ring of bwd_ring(QB) stages in the LDS, one barrier per stage:
-// it shows the stage complete (each loader has waited for its own loads) and
-// every wavefront done with the slot the loaders refill next.
-template <int OP, int QB, bool LOADER, int WQ, bool NT>
-__device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile& t, lds_t* lds) {
-  constexpr bool PS = p_strided(OP), QS = q_strided(OP);
-  constexpr int NM = (QB + 1 - WQ) / 2, NIQ = QS ? 8 : QB, LD = 8 + NIQ;
-  constexpr int S = bwd_ring(QB), SB = kStageP + stage_q(QB);
-  static_assert(!QS || QB == 8, "a strided Q side has 256 columns");
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w >> 1, lw = w - 4;
-  f32x16 acc[NM][2];
+template <int NM, int NB>
+__device__ __forceinline__ void clear_acc(f32x16 (&acc)[NM][NB]) {
 #pragma unroll
   for (int a = 0; a < NM; ++a)
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
+}
+
+// Wait until at most min(N, n) stages of LD loads are in flight.
+template <int LD, int N>
+__device__ __forceinline__ void wait_stages(int n) {
+  if constexpr (N == 0) wait_vmcnt<0>();
+  else if (n >= N) wait_vmcnt<N * LD>();
+  else wait_stages<LD, N - 1>(n);
+}
+
+// A tile of GU, DACT or DX. A ring of bwd_ring() stages in the LDS, one barrier
+// per stage: it shows the stage complete (each loader has waited for its own
+// loads) and every wavefront done with the slot the loaders refill next.
+template <int OP, int PB, int QB, bool LOADER, int WQ, bool NT>
+__device__ __forceinline__ void band_tile_body(const BwdParams& P, const BwdTile& t, lds_t* lds) {
+  constexpr bool PS = p_strided(OP);
+  constexpr int NM = (QB + 1 - WQ) / 2, NB = PB / 4, LD = PB + QB;
+  constexpr int S = bwd_ring(PB, QB), SB = stage_bytes_of(PB + QB);
+  static_assert(S >= 2 && (S - 2) * LD < 64, "ring depth");
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w >> 1, lw = w - 4;
+  f32x16 acc[NM][NB];
+  clear_acc(acc);
 
   const int KT = t.ktiles;
-  Loads<PS, 8> lp;
-  Loads<QS, NIQ> lq;
+  WeightLoads<PS, PB, NT> lp;
+  BandLoads<QB> lq;
   auto issue = [&](int stage, int slot) {
-    int kt = stage;
-    if constexpr (!QS) kt = stage + t.krot >= KT ? stage + t.krot - KT : stage + t.krot;
-    lp.template issue<NT>(kt, lds + slot * SB, lw, lane);
-    lq.template issue<false>(kt, lds + slot * SB + kStageP, lw, lane);
+    const int kt = stage + t.krot >= KT ? stage + t.krot - KT : stage + t.krot;
+    lp.issue(kt, lds + slot * SB, lw, lane);
+    lq.issue(kt, lds + slot * SB + stage_bytes_of(PB), lw, lane);
   };
   if constexpr (LOADER) {
-    lp.init(t.P, lw, lane, true);
-    lq.init(t.Q, lw, lane, false);
+    lp.init(t.P, lw, lane);
+    lq.init(t.Q, lw, lane);
 #pragma unroll
     for (int s = 0; s < S - 1; ++s)
       if (s < KT) issue(s, s);
   }
   int rd = 0, wr = S - 1;
   for (int kt = 0; kt < KT; ++kt) {
-    if constexpr (LOADER) {
-      // the stages after kt that are in flight: S - 2, near the end fewer
-      const int after = KT - 1 - kt;
-      if (after >= S - 2) wait_vmcnt<(S - 2) * LD>();
-      else if (S > 3 && after == 1) wait_vmcnt<LD>();
-      else wait_vmcnt<0>();
-    }
+    if constexpr (LOADER) wait_stages<LD, S - 2>(KT - 1 - kt);
     lds_barrier();
-    lds_t* st = lds + rd * SB;
-    if constexpr (QS) {
-      // K rows past the expert's last: zero on both sides
-      const int left = t.P.valid - kt * kBK;
-      if (left < kBK) {
-        for (int i = left * 32 + tid; i < kBK * 32; i += kBwdThreads) {
-          *(lds_i32x4*)(st + i * 16) = i32x4{0, 0, 0, 0};
-          *(lds_i32x4*)(st + kStageP + i * 16) = i32x4{0, 0, 0, 0};
-        }
-        lds_barrier();
-      }
-    }
-    bwd_stage<PS, QS, NM>(st, WQ, wp, lane, acc, [&]() {
+    bwd_stage<PS, false, PB, QB, NM>(lds + rd * SB, WQ, wp, lane, acc, [&]() {
       if constexpr (LOADER) {
         if (kt + S - 1 < KT) issue(kt + S - 1, wr);
       }
@@ -383,41 +401,42 @@ __device__ __forceinline__ void bwd_tile_body(const BwdParams& P, const BwdTile&
       dst[a] = m < t.rows ? P.row_dst[t.row0 + m] : 0;
     }
   }
-  if (wp * 64 < t.cols) {
+  if (wp * (NB * 32) < t.cols) {
 #pragma unroll
     for (int a = 0; a < NM; ++a) {
       const int m0 = (WQ + 2 * a) * 32;
-      if (m0 < t.rows) store_block<OP>(P, t, lds + w * 8192, acc[a], m0, wp * 64, OP == BWD_DX ? dst[a] : 0, lane);
+      if (m0 < t.rows)
+        store_block<OP, NB>(P, t, lds + w * 8192, acc[a], m0, wp * (NB * 32), OP == BWD_DX ? dst[a] : 0, lane);
     }
   }
   lds_barrier();  // ... for the next tile's loads
 }
 
 // A wavefront's role: loader or not, and its row of the 2 x 4 wavefront grid.
-template <int OP, int QB, bool NT>
-__device__ __forceinline__ void run_bwd_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
+template <int OP, int PB, int QB, bool NT>
+__device__ __forceinline__ void run_roles(const BwdParams& P, const BwdTile& t, lds_t* lds) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (w >= 8 - kLoaders) {
-    if (w & 1) bwd_tile_body<OP, QB, true, 1, NT>(P, t, lds);
-    else bwd_tile_body<OP, QB, true, 0, NT>(P, t, lds);
+    if (w & 1) band_tile_body<OP, PB, QB, true, 1, NT>(P, t, lds);
+    else band_tile_body<OP, PB, QB, true, 0, NT>(P, t, lds);
   } else {
-    if (w & 1) bwd_tile_body<OP, QB, false, 1, NT>(P, t, lds);
-    else bwd_tile_body<OP, QB, false, 0, NT>(P, t, lds);
+    if (w & 1) band_tile_body<OP, PB, QB, false, 1, NT>(P, t, lds);
+    else band_tile_body<OP, PB, QB, false, 0, NT>(P, t, lds);
   }
 }
 
-template <int OP, bool NT>
+template <int OP, int PB, bool NT>
 __device__ __forceinline__ void run_band_tile(const BwdParams& P, const BwdTile& t, lds_t* lds) {
-  if (t.rows <= 64) run_bwd_tile<OP, 2, NT>(P, t, lds);
-  else if (t.rows <= 128) run_bwd_tile<OP, 4, NT>(P, t, lds);
-  else if (t.rows <= 160) run_bwd_tile<OP, 5, NT>(P, t, lds);
-  else if (t.rows <= 192) run_bwd_tile<OP, 6, NT>(P, t, lds);
-  else run_bwd_tile<OP, 8, NT>(P, t, lds);
+  if (t.rows <= 64) run_roles<OP, PB, 2, NT>(P, t, lds);
+  else if (t.rows <= 128) run_roles<OP, PB, 4, NT>(P, t, lds);
+  else if (t.rows <= 160) run_roles<OP, PB, 5, NT>(P, t, lds);
+  else if (t.rows <= 192) run_roles<OP, PB, 6, NT>(P, t, lds);
+  else run_roles<OP, PB, 8, NT>(P, t, lds);
 }
 
-// Tile (p, n) of GU, DACT or DX: row band p, column tile n.
+// Tile (p, n) of GU, DACT or DX: row band p, column tile n of `width` columns.
 template <int OP>
-__device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n) {
+__device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n, int width) {
   BwdTile t;
   t.e = P.band_expert[p] & kBandExpertMask;
   // bands of different experts run together: DACT starts their K slices apart,
@@ -426,25 +445,25 @@ __device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n) {
   const bool once = (P.band_expert[p] & kBandSingle) != 0;
   t.row0 = P.band_row0[p];
   t.rows = P.band_rows[p];
-  t.col0 = n * kTP;
+  t.col0 = n * width;
   const uint32_t db = (uint32_t)P.d * 2, fb = (uint32_t)P.f * 2;
   const uint8_t* w1 = P.W1 + (size_t)t.e * (2 * (size_t)P.f) * db;
   const uint8_t* w2 = P.W2 + (size_t)t.e * (size_t)P.d * fb;
   if constexpr (OP == BWD_GU) {
-    t.cols = min(kTP, 2 * P.f - t.col0);
+    t.cols = min(width, 2 * P.f - t.col0);
     t.ktiles = P.d / kBK;
     t.krot = 0;
     t.P = Side{w1 + (size_t)t.col0 * db, db, t.cols, 0, nullptr, 1};
     t.Q = P.row_src ? Side{P.X, db, t.rows, 0, P.row_src + t.row0, P.k}
                     : Side{P.X + (size_t)t.row0 * db, db, t.rows, 0, nullptr, 1};
   } else if constexpr (OP == BWD_DACT) {
-    t.cols = min(kTP, P.f - t.col0);
+    t.cols = min(width, P.f - t.col0);
     t.ktiles = P.d / kBK;
     t.krot = once ? t.e * kKRot % t.ktiles : 0;
     t.P = Side{w2 + (size_t)t.col0 * 2, fb, P.d, t.cols / 8, nullptr, 1};
     t.Q = Side{P.dO, db, t.rows, 0, P.row_dst + t.row0, 1};
   } else {
-    t.cols = min(kTP, P.d - t.col0);
+    t.cols = min(width, P.d - t.col0);
     t.ktiles = 2 * P.f / kBK;
     t.krot = 0;
     t.P = Side{w1 + (size_t)t.col0 * 2, db, 2 * P.f, t.cols / 8, nullptr, 1};
@@ -462,8 +481,8 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
   const int M = OP == BWD_DW2 ? P.d : 2 * P.f, N = OP == BWD_DW2 ? P.f : P.d;
   t.row0 = m * kBM;
   t.rows = min(kBM, M - t.row0);
-  t.col0 = n * kTP;
-  t.cols = min(kTP, N - t.col0);
+  t.col0 = n * 256;
+  t.cols = min(256, N - t.col0);
   t.ktiles = (cnt + kBK - 1) / kBK;
   const uint32_t db = (uint32_t)P.d * 2, fb = (uint32_t)P.f * 2;
   if constexpr (OP == BWD_DW2) {
@@ -479,6 +498,92 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
   return t;
 }
 
+// DW1 or DW2: a workgroup's tiles, one after the other. The tiles are short in
+// K (the expert's rows: two or three stages on the share) and long in stores
+// (128 KiB), so a tile's first two stages are loaded while its predecessor's
+// results are still being stored, which go through LDS of their own (4 KiB per
+// wavefront behind the two-stage ring).
+// The loader's wait for stage kt: vmcnt counts loads and stores in order, 16 or
+// more loads of stage 1 stand behind stage 0, and behind stage 1 the 16 stores
+// per wavefront of a full predecessor (`full`).
+template <int OP, bool LOADER, int WQ>
+__device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds, int lid, int G) {
+  constexpr int SB = stage_bytes_of(16);
+  static_assert(2 * SB + 8 * 4096 <= kGemmLds, "ring and store buffers");
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w >> 1, lw = w - 4;
+  const int M = ((OP == BWD_DW2 ? P.d : 2 * P.f) + 255) / 256, N = ((OP == BWD_DW2 ? P.f : P.d) + 255) / 256;
+  const int64_t total = (int64_t)P.El * M * N;
+  auto tile_at = [&](int64_t i) {
+    const int e = (int)(i / (M * N));
+    int m, n;
+    raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
+    return weight_tile<OP>(P, e, m, n);
+  };
+  RowLoads lp, lq;
+  auto issue = [&](int kt, int slot) {
+    lp.issue(kt, lds + slot * SB, lw, lane);
+    lq.issue(kt, lds + slot * SB + SB / 2, lw, lane);
+  };
+  auto start = [&](const BwdTile& t, bool same_expert) {
+    if constexpr (LOADER) {
+      lp.init(t.P, lw, lane, same_expert);
+      lq.init(t.Q, lw, lane, same_expert);
+      if (t.ktiles > 0) issue(0, 0);
+      if (t.ktiles > 1) issue(1, 1);
+    }
+  };
+  if (lid >= total) return;
+  BwdTile t = tile_at(lid);
+  start(t, false);
+  bool full = false;
+  for (int64_t i = lid;;) {
+    f32x16 acc[4][2];
+    clear_acc(acc);
+    for (int kt = 0; kt < t.ktiles; ++kt) {
+      if constexpr (LOADER) {
+        if ((kt == 0 && t.ktiles > 1) || (kt < 2 && full)) wait_vmcnt<16>();
+        else wait_vmcnt<0>();
+      }
+      lds_barrier();
+      lds_t* st = lds + (kt & 1) * SB;
+      // K rows past the expert's last: zero on both sides
+      const int left = t.P.valid - kt * kBK;
+      if (left < kBK) {
+        for (int c = left * 32 + tid; c < kBK * 32; c += kBwdThreads) {
+          *(lds_i32x4*)(st + c * 16) = i32x4{0, 0, 0, 0};
+          *(lds_i32x4*)(st + SB / 2 + c * 16) = i32x4{0, 0, 0, 0};
+        }
+        lds_barrier();
+      }
+      bwd_stage<true, true, 8, 8, 4>(st, WQ, wp, lane, acc, [&]() {
+        if constexpr (LOADER) {
+          if (kt > 0 && kt + 1 < t.ktiles) issue(kt + 1, (kt + 1) & 1);
+        }
+      });
+    }
+    lds_barrier();  // the ring is free
+    i += G;
+    const bool more = i < total;
+    BwdTile next;
+    if (more) {
+      next = tile_at(i);
+      start(next, next.e == t.e);
+    }
+    if (wp * 64 < t.cols) {
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const int m0 = (WQ + 2 * a) * 32;
+        if (m0 < t.rows) store_block<OP, 2>(P, t, lds + 2 * SB + w * 4096, acc[a], m0, wp * 64, 0, lane);
+      }
+    }
+    if (!more) break;
+    full = t.rows == 256 && t.cols == 256;
+    t = next;
+  }
+}
+
 template <int OP>
 __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kGemmLds];
@@ -490,24 +595,34 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
   if constexpr (OP <= BWD_DX) {
     const int nb = P.meta[META_P];
     const int width = OP == BWD_GU ? 2 * P.f : OP == BWD_DACT ? P.f : P.d;
-    const int N = (width + kTP - 1) / kTP;
-    for (int i = lid; i < nb * N; i += G) {
+    const int N = (width + 255) / 256, total = nb * N, cut = total / G * G;
+    // whole rounds of 256-column tiles, then the rest as halves
+    for (int i = lid; i < cut + 2 * (total - cut); i += G) {
+      const bool wide = i < cut;
       int p, n;
-      raster(i, nb, N, P.group_m, p, n);
-      const BwdTile t = band_tile<OP>(P, p, n);
+      raster(wide ? i : cut + ((i - cut) >> 1), nb, N, P.group_m, p, n);
+      if (!wide) n = 2 * n + ((i - cut) & 1);
+      const BwdTile t = band_tile<OP>(P, p, n, wide ? 256 : 128);
+      if (t.cols <= 0) continue;
       // weights of an expert with one band are read once per launch (see
       // streams_once)
-      if (P.band_expert[p] & kBandSingle) run_band_tile<OP, true>(P, t, lds);
-      else run_band_tile<OP, false>(P, t, lds);
+      const bool once = (P.band_expert[p] & kBandSingle) != 0;
+      if (wide) {
+        if (once) run_band_tile<OP, 8, true>(P, t, lds);
+        else run_band_tile<OP, 8, false>(P, t, lds);
+      } else {
+        if (once) run_band_tile<OP, 4, true>(P, t, lds);
+        else run_band_tile<OP, 4, false>(P, t, lds);
+      }
     }
   } else {
-    const int M = ((OP == BWD_DW2 ? P.d : 2 * P.f) + kBM - 1) / kBM;
-    const int N = ((OP == BWD_DW2 ? P.f : P.d) + kTP - 1) / kTP;
-    for (int64_t i = lid; i < (int64_t)P.El * M * N; i += G) {
-      const int e = (int)(i / (M * N));
-      int m, n;
-      raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
-      run_bwd_tile<OP, 8, false>(P, weight_tile<OP>(P, e, m, n), lds);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (w >= 8 - kLoaders) {
+      if (w & 1) weight_tiles_body<OP, true, 1>(P, lds, lid, G);
+      else weight_tiles_body<OP, true, 0>(P, lds, lid, G);
+    } else {
+      if (w & 1) weight_tiles_body<OP, false, 1>(P, lds, lid, G);
+      else weight_tiles_body<OP, false, 0>(P, lds, lid, G);
     }
   }
 }

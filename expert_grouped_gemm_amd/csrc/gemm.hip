@@ -19,33 +19,110 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
             band_row0, band_rows, l2_full, wave_band0, meta);
 }
 
-// The plan for calls whose row indices come from the caller: row_src entries
-// outside [0, src_end) or row_dst entries outside [0, cap), among the rows the
-// offsets cover, empty the plan like bad offsets do (no tile runs, nothing is
-// read through them) and set their error bits. Either array may be null. One
-// block reads them all: 131072 rows are 128 coalesced loads per thread.
-__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap, int N1,
-                                                         int G, int Pmax, const int32_t* __restrict__ row_src,
-                                                         int64_t src_end, const int32_t* __restrict__ row_dst,
+// The plan for calls with their own offsets and row indices (the MXFP4
+// Linears and the experts' gradient): the row-band table alone, as those
+// calls run the separate schedule's order. Thread e handles expert e. Full
+// bands of 256 rows come first, then the experts' last, shorter ones by their
+// 32-row blocks, largest first (see plan_body). Offsets are checked as there;
+// row_src entries outside [0, src_end) or row_dst entries outside [0, cap),
+// among the rows the offsets cover, empty the plan as well (no tile runs,
+// nothing is read through them) and set their error bits. Either array may be
+// null. One block: the whole of plan_body plus these checks took 12 us on the
+// share (4096 rows, 32 experts), this takes 5.
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap,
+                                                         const int32_t* __restrict__ row_src, int64_t src_end,
+                                                         const int32_t* __restrict__ row_dst,
                                                          int32_t* __restrict__ band_expert,
                                                          int32_t* __restrict__ band_row0,
-                                                         int32_t* __restrict__ band_rows,
-                                                         int32_t* __restrict__ l2_full,
-                                                         int32_t* __restrict__ wave_band0, int32_t* __restrict__ meta) {
-  plan_body(offsets, El, cap, N1, G, 0, 1, Pmax, ARG_ERR_ALL, nullptr, 0, band_expert, band_row0, band_rows, l2_full,
-            wave_band0, meta);
-  const int lo = max(0, offsets[0]), hi = min(cap, offsets[El]);
-  bool bad_src = false, bad_dst = false;
-#pragma unroll 4
-  for (int r = lo + (int)threadIdx.x; r < hi; r += 1024) {
-    if (row_src) bad_src |= row_src[r] < 0 || row_src[r] >= src_end;
-    if (row_dst) bad_dst |= (unsigned)row_dst[r] >= (unsigned)cap;
+                                                         int32_t* __restrict__ band_rows, int32_t* __restrict__ meta) {
+  // per wavefront: last bands of each class, and full bands; then the sums
+  // over the wavefronts before it, the totals in row `waves`
+  __shared__ int wave_sum[17][9];
+  __shared__ int err;
+  const int e = threadIdx.x, lane = e & 63, wv = e >> 6, waves = blockDim.x >> 6;
+  if (e == 0) err = 0;
+  const int lo = e < El ? offsets[e] : 0, hi = e < El ? offsets[e + 1] : 0;
+  const int first = offsets[0], last = offsets[El];
+  __syncthreads();
+  int bits = hi < lo || first < 0 || last > cap ? ARG_ERR_OFFSETS : 0;
+  const int r_end = min(cap, last);
+  for (int r = max(0, first) + e; r < r_end; r += 4 * (int)blockDim.x) {
+    int src[4], dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = min(r + (int)blockDim.x * i, r_end - 1);
+      src[i] = row_src ? row_src[q] : 0;
+      dst[i] = row_dst ? row_dst[q] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (src[i] < 0 || src[i] >= src_end) bits |= ARG_ERR_ROW_SRC;
+      if ((unsigned)dst[i] >= (unsigned)cap) bits |= ARG_ERR_ROW_DST;
+    }
   }
-  const int any_src = __syncthreads_or(bad_src), any_dst = __syncthreads_or(bad_dst);
-  if (threadIdx.x == 0 && (any_src || any_dst)) {
-    meta[META_P] = 0;
-    __hip_atomic_fetch_or(meta + META_ARG_ERR, (any_src ? ARG_ERR_ROW_SRC : 0) | (any_dst ? ARG_ERR_ROW_DST : 0),
-                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (bits) atomicOr(&err, bits);
+  // ranks: the full bands of the experts before this one, and the experts
+  // before it (in this wavefront; those of other wavefronts below) with a last
+  // band of its class
+  const int full = (hi - lo) / kBM, rest = (hi - lo) % kBM;
+  const int cls = rest ? 8 - ((rest + 31) >> 5) : -1;
+  int scan = full;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(scan, off, 64);
+    if (lane >= off) scan += y;
+  }
+  if (lane == 63) wave_sum[wv][8] = scan;
+  uint64_t mine = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint64_t bal = __ballot(cls == c);
+    if (lane == c) wave_sum[wv][c] = __popcll(bal);
+    if (cls == c) mine = bal;
+  }
+  __syncthreads();
+  if (e == 0) {
+    meta[META_ERR] = 0;
+    meta[META_TRACE_N] = 0;
+    meta[META_ARG_ERR] = err;
+  }
+  if (err) {
+    if (e == 0) meta[META_P] = meta[META_A] = 0;
+    return;
+  }
+  if (e < 9) {
+    int sum = 0;
+    for (int i = 0; i < waves; ++i) {
+      const int n = wave_sum[i][e];
+      wave_sum[i][e] = sum;
+      sum += n;
+    }
+    wave_sum[waves][e] = sum;
+  }
+  __syncthreads();
+  const int full_before = wave_sum[wv][8] + scan - full, full_all = wave_sum[waves][8];
+  int cls_before = __popcll(mine & ((1ull << lane) - 1ull)), parts = 0;
+  if (rest) cls_before += wave_sum[wv][cls];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    if (c < cls) cls_before += wave_sum[waves][c];
+    parts += wave_sum[waves][c];
+  }
+  const int single = hi - lo <= kBM ? kBandSingle : 0;
+  for (int i = 0; i < full; ++i) {
+    band_expert[full_before + i] = e | single;
+    band_row0[full_before + i] = lo + i * kBM;
+    band_rows[full_before + i] = kBM;
+  }
+  if (rest) {
+    const int at = full_all + cls_before;
+    band_expert[at] = e | single;
+    band_row0[at] = lo + full * kBM;
+    band_rows[at] = rest;
+  }
+  if (e == 0) {
+    meta[META_P] = full_all + parts;
+    meta[META_A] = last;
   }
 }
 
@@ -54,9 +131,10 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
 hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
                             const int32_t* row_src, const int32_t* row_dst, hipStream_t s) {
   auto I = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(1024), 0, s, offsets, L.E_l, L.cap, 1, 1, L.Pmax, row_src,
-                     (int64_t)p.T * p.k, row_dst, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.l2_full),
-                     I(L.wave_band0), I(L.pub.meta));
+  // a thread per expert at least; enough of them for the row indices
+  const int threads = L.E_l > 256 || L.cap > 65536 ? 1024 : 256;
+  hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(threads), 0, s, offsets, L.E_l, L.cap, row_src, (int64_t)p.T * p.k,
+                     row_dst, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.pub.meta));
   return hipGetLastError();
 }
 

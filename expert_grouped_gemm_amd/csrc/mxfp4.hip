@@ -87,10 +87,10 @@ __global__ __launch_bounds__(256) void mxfp4_dequantize_kernel(const uint32_t* _
       dst[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
       uint4 o;
-      o.x = f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16);
-      o.y = f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16);
-      o.z = f32_to_bf16_rne(v[4]) | ((uint32_t)f32_to_bf16_rne(v[5]) << 16);
-      o.w = f32_to_bf16_rne(v[6]) | ((uint32_t)f32_to_bf16_rne(v[7]) << 16);
+      o.x = pack_bf16(v[0], v[1]);
+      o.y = pack_bf16(v[2], v[3]);
+      o.z = pack_bf16(v[4], v[5]);
+      o.w = pack_bf16(v[6], v[7]);
       static_cast<uint4*>(out)[i] = o;
     }
   }
