@@ -54,6 +54,8 @@ __host__ __device__ constexpr int bwd_ring(int PB, int QB) {
   return s > 6 ? 6 : s;
 }
 
+constexpr int kShortRows = 512;              // rows per expert up to which weight_backward_short_kernel runs
+
 struct BwdParams {
   const uint8_t* X;          // token rows [T, d] (through row_src) or expert-ordered rows
   const uint8_t* dO;         // [cap, d], row r at slot row_dst[r]
@@ -92,6 +94,31 @@ struct Side {
 // go to the four 64-byte quarters of a bank line.
 __device__ __forceinline__ int ks_swizzle(int kk) { return (kk & 3) << 2; }
 
+// One direct global -> LDS load of 16 bytes per lane: lane l's bytes at base +
+// off land at st + 16 l. Written out because the compiler, which cannot tell
+// the transposing LDS reads that follow from the bytes still under way, waits
+// for every load it issued through the builtin before the next such read:
+// the loaders then stood still in every stage until the next stage's data had
+// come, and the ring overlapped nothing. The load has no register result; its
+// completion is waited for in wait_vmcnt() before the barrier that publishes
+// the stage.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // M0 is reserved, and named as overwritten
+template <bool NT>
+__device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, lds_t* st) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);  // a uniform value, as the instruction's scalar base
+  const uint64_t sb = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b) |
+                      ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32);
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)st);
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(m0), "v"(off), "s"(sb)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(sb)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // The ring's loads of one side, as one loader wavefront issues them: NI
 // instructions of 1 KiB per stage. An instruction takes 8 rows of 128 bytes
 // (KC), 2 K rows of 512 bytes or 4 of 256 (KS); loader lw of 4 takes
@@ -124,8 +151,7 @@ struct WeightLoads {
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int step = KS || j * 4 * RPI < valid ? j : j - NI / 2;
-      __builtin_amdgcn_global_load_lds(b0 + (size_t)step * (4 * RPI) * pitch + lane_off, st + (4 * j + lw) * 1024, 16, 0,
-                                       NT ? kCpolNT : 0);
+      dma16<NT>(b0 + (size_t)step * (4 * RPI) * pitch, lane_off, st + (4 * j + lw) * 1024);
     }
   }
 };
@@ -149,25 +175,27 @@ struct BandLoads {
   __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int) {
     const uint8_t* b0 = base + (size_t)kt * (kBK * 2);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) __builtin_amdgcn_global_load_lds(b0 + off[j], st + (4 * j + lw) * 1024, 16, 0, 0);
+    for (int j = 0; j < NI; ++j) dma16<false>(b0, off[j], st + (4 * j + lw) * 1024);
   }
 };
 
-// An expert's rows as K (KS, 256 columns), perhaps through idx. Lane kk looks
-// up K row kk of a stage for all lanes; rows past the last re-read it (the
-// stage's LDS rows are zeroed). The first two stages' rows are kept while the
-// expert stays, so that the next tile's first loads wait for no index; later
-// stages' are fetched when the stage before is issued.
+// An expert's rows as K (KS), BK of them a stage, perhaps through idx. Lane kk
+// keeps the offset of K row kk of the stage for all lanes; rows past the last
+// re-read it (the stage's LDS rows are zeroed). With idx, the first two stages'
+// rows are kept while the expert stays, so that the next tile's first loads
+// wait for no index; later stages' are fetched when the stage before is issued.
+// Offsets through idx fit 32 bits (the problem limits keep T * d and cap * d
+// below 2^31 elements); without, they count from the stage's first row.
+template <int BLOCKS, int BK>
 struct RowLoads {
-  static constexpr int NI = 8;
+  static constexpr int CPR = BLOCKS * 4, RPI = 64 / CPR, NI = BK * BLOCKS / 64;
   const uint8_t* base;
-  uint32_t pitch, lane_off;
+  uint32_t pitch, lane_off, r0, r1, next;
   const int32_t* idx;
-  int div, valid, r0, r1, next;
+  int div, valid;
 
-  __device__ __forceinline__ int look_up(int kt, int lane) const {
-    const int row = min(kt * kBK + lane, valid - 1);
-    return idx ? idx[row] / div : row;
+  __device__ __forceinline__ uint32_t look_up(int kt, int lane) const {
+    return (uint32_t)(idx[min(kt * BK + (lane & (BK - 1)), valid - 1)] / div) * pitch;
   }
   __device__ __forceinline__ void init(const Side& s, int lw, int lane, bool same_expert) {
     base = s.base;
@@ -175,23 +203,28 @@ struct RowLoads {
     idx = s.idx;
     div = s.div;
     valid = s.valid;
-    const int kk = 2 * lw + (lane >> 5);
-    lane_off = (((lane & 31) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
-    if (!same_expert && valid > 0) {
+    const int kk = lw * RPI + lane / CPR;
+    lane_off = (((lane % CPR) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
+    if (idx && !same_expert && valid > 0) {
       r0 = look_up(0, lane);
       r1 = look_up(1, lane);
     }
   }
   __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
-    const int rows = kt == 0 ? r0 : kt == 1 ? r1 : next;
-    if (kt > 0 && (kt + 1) * kBK < valid) next = look_up(kt + 1, lane);
+    const int kk = lw * RPI + lane / CPR, left = valid - kt * BK;
+    const uint8_t* b0 = idx ? base : base + (size_t)kt * BK * pitch;
+    if (!idx && left >= BK) {
+      const uint32_t off = kk * pitch + lane_off;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int a = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw);
-      const int b = __builtin_amdgcn_readlane(rows, 8 * j + 2 * lw + 1);
-      __builtin_amdgcn_global_load_lds(base + (size_t)(lane < 32 ? a : b) * pitch + lane_off, st + (4 * j + lw) * 1024,
-                                       16, 0, 0);
+      for (int j = 0; j < NI; ++j)
+        dma16<false>(b0 + (size_t)(4 * j * RPI) * pitch, off, st + (4 * j + lw) * 1024);
+      return;
     }
+    const uint32_t rows = !idx ? min(lane & (BK - 1), left - 1) * pitch : kt == 0 ? r0 : kt == 1 ? r1 : next;
+    if (idx && kt > 0 && left > BK) next = look_up(kt + 1, lane);
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+      dma16<false>(b0, (uint32_t)__shfl((int)rows, 4 * j * RPI + kk, 64) + lane_off, st + (4 * j + lw) * 1024);
   }
 };
 
@@ -305,10 +338,10 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
   wave_lds_sync();
 }
 
-// One stage: MFMAs of a wavefront that owns NM Q blocks wq, wq + 2, ... and the
+// One stage: MFMAs of a wavefront that owns NM Q blocks wq, wq + QSTEP, ... and the
 // P blocks from wp * PB / 4 on. The fragments of step ks + 1 are read before
 // the MFMAs of step ks; issue() issues the loader's loads behind the first.
-template <bool PS, bool QS, int PB, int QB, int NM, class Issue>
+template <bool PS, bool QS, int PB, int QB, int NM, int BK = kBK, int QSTEP = 2, class Issue>
 __device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int lane, f32x16 (&acc)[NM][PB / 4],
                                           const Issue& issue) {
   constexpr int NB = PB / 4;
@@ -317,12 +350,12 @@ __device__ __forceinline__ void bwd_stage(const lds_t* st, int wq, int wp, int l
 #pragma unroll
     for (int b = 0; b < NB; ++b) fp[buf][b] = fragment<PS, PB>(st, NB * wp + b, ks, lane);
 #pragma unroll
-    for (int a = 0; a < NM; ++a) fq[buf][a] = fragment<QS, QB>(st + stage_bytes_of(PB), wq + 2 * a, ks, lane);
+    for (int a = 0; a < NM; ++a) fq[buf][a] = fragment<QS, QB>(st + PB * 64 * BK, wq + QSTEP * a, ks, lane);
   };
   read(0, 0);
 #pragma unroll
-  for (int ks = 0; ks < kBK / 16; ++ks) {
-    if (ks + 1 < kBK / 16) read(ks + 1, (ks + 1) & 1);
+  for (int ks = 0; ks < BK / 16; ++ks) {
+    if (ks + 1 < BK / 16) read(ks + 1, (ks + 1) & 1);
     if (ks == 0) issue();
 #pragma unroll
     for (int a = 0; a < NM; ++a)
@@ -472,18 +505,18 @@ __device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n, i
   return t;
 }
 
-// Tile (m, n) of an expert's weight gradient.
+// Tile (m, n) of an expert's weight gradient, TM rows high.
 template <int OP>
-__device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m, int n) {
+__device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m, int n, int TM) {
   BwdTile t;
   t.e = e;
   const int r0 = P.offsets[e], cnt = P.offsets[e + 1] - r0;
   const int M = OP == BWD_DW2 ? P.d : 2 * P.f, N = OP == BWD_DW2 ? P.f : P.d;
-  t.row0 = m * kBM;
-  t.rows = min(kBM, M - t.row0);
+  t.row0 = m * TM;
+  t.rows = min(TM, M - t.row0);
   t.col0 = n * 256;
   t.cols = min(256, N - t.col0);
-  t.ktiles = (cnt + kBK - 1) / kBK;
+  t.ktiles = TM == 256 ? (cnt + 63) / 64 : (cnt + 31) / 32;
   const uint32_t db = (uint32_t)P.d * 2, fb = (uint32_t)P.f * 2;
   if constexpr (OP == BWD_DW2) {
     t.P = Side{reinterpret_cast<const uint8_t*>(P.act) + (size_t)r0 * fb + (size_t)t.col0 * 2, fb, cnt, t.cols / 8,
@@ -498,33 +531,42 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
   return t;
 }
 
-// DW1 or DW2: a workgroup's tiles, one after the other. The tiles are short in
-// K (the expert's rows: two or three stages on the share) and long in stores
-// (128 KiB), so a tile's first two stages are loaded while its predecessor's
-// results are still being stored, which go through LDS of their own (4 KiB per
-// wavefront behind the two-stage ring).
-// The loader's wait for stage kt: vmcnt counts loads and stores in order, 16 or
-// more loads of stage 1 stand behind stage 0, and behind stage 1 the 16 stores
-// per wavefront of a full predecessor (`full`).
-template <int OP, bool LOADER, int WQ>
+// DW1 or DW2: a workgroup's tiles, one after the other. A tile's first two
+// stages are loaded while its predecessor's results are still being stored,
+// which go through LDS of their own (4 KiB per wavefront behind the two-stage
+// ring).
+// WAVES = 8: 256 x 256 tiles, 64 K rows a stage, one workgroup per CU, the
+// last four wavefronts load. WAVES = 4: 128 x 256 tiles, 32 K rows a stage, two
+// workgroups per CU (72 KiB of LDS each), every wavefront loads: for experts
+// of few rows, whose tiles are a few stages long and otherwise stores, setup and
+// waits, which the two workgroups overlap.
+// The loader's wait for stage kt: vmcnt counts loads and stores in order; the
+// LD or more loads of stage 1 stand behind stage 0, and behind stage 1 the 16
+// stores per wavefront of a full predecessor (`full`).
+template <int OP, int WAVES, bool LOADER, int WQ>
 __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds, int lid, int G) {
-  constexpr int SB = stage_bytes_of(16);
-  static_assert(2 * SB + 8 * 4096 <= kGemmLds, "ring and store buffers");
+  constexpr int QB = WAVES, BK = WAVES == 8 ? 64 : 32, NW = WAVES / 4, TM = QB * 32;
+  constexpr int SB = (8 + QB) * 64 * BK;  // stage bytes: 64 of each block per K row
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w >> 1, lw = w - 4;
-  const int M = ((OP == BWD_DW2 ? P.d : 2 * P.f) + 255) / 256, N = ((OP == BWD_DW2 ? P.f : P.d) + 255) / 256;
+  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w / NW, lw = w - (WAVES - 4);
+  const int M = (OP == BWD_DW2 ? P.d : 2 * P.f) / TM + ((OP == BWD_DW2 ? P.d : 2 * P.f) % TM != 0);
+  const int N = ((OP == BWD_DW2 ? P.f : P.d) + 255) / 256;
   const int64_t total = (int64_t)P.El * M * N;
   auto tile_at = [&](int64_t i) {
     const int e = (int)(i / (M * N));
     int m, n;
     raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
-    return weight_tile<OP>(P, e, m, n);
+    return weight_tile<OP>(P, e, m, n, TM);
   };
-  RowLoads lp, lq;
+  typedef RowLoads<8, BK> LoadsP;
+  typedef RowLoads<QB, BK> LoadsQ;
+  constexpr int LD = LoadsP::NI + LoadsQ::NI;
+  LoadsP lp;
+  LoadsQ lq;
   auto issue = [&](int kt, int slot) {
     lp.issue(kt, lds + slot * SB, lw, lane);
-    lq.issue(kt, lds + slot * SB + SB / 2, lw, lane);
+    lq.issue(kt, lds + slot * SB + 8 * 64 * BK, lw, lane);
   };
   auto start = [&](const BwdTile& t, bool same_expert) {
     if constexpr (LOADER) {
@@ -543,21 +585,21 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
     clear_acc(acc);
     for (int kt = 0; kt < t.ktiles; ++kt) {
       if constexpr (LOADER) {
-        if ((kt == 0 && t.ktiles > 1) || (kt < 2 && full)) wait_vmcnt<16>();
+        if (kt == 0 && t.ktiles > 1) wait_vmcnt<LD>();
+        else if (kt < 2 && full) wait_vmcnt<16>();
         else wait_vmcnt<0>();
       }
       lds_barrier();
       lds_t* st = lds + (kt & 1) * SB;
       // K rows past the expert's last: zero on both sides
-      const int left = t.P.valid - kt * kBK;
-      if (left < kBK) {
-        for (int c = left * 32 + tid; c < kBK * 32; c += kBwdThreads) {
-          *(lds_i32x4*)(st + c * 16) = i32x4{0, 0, 0, 0};
-          *(lds_i32x4*)(st + SB / 2 + c * 16) = i32x4{0, 0, 0, 0};
-        }
+      const int left = t.P.valid - kt * BK;
+      if (left < BK) {
+        for (int c = left * 32 + tid; c < BK * 32; c += WAVES * 64) *(lds_i32x4*)(st + c * 16) = i32x4{0, 0, 0, 0};
+        for (int c = left * (QB * 4) + tid; c < BK * (QB * 4); c += WAVES * 64)
+          *(lds_i32x4*)(st + 8 * 64 * BK + c * 16) = i32x4{0, 0, 0, 0};
         lds_barrier();
       }
-      bwd_stage<true, true, 8, 8, 4>(st, WQ, wp, lane, acc, [&]() {
+      bwd_stage<true, true, 8, QB, 4, BK, NW>(st, WQ, wp, lane, acc, [&]() {
         if constexpr (LOADER) {
           if (kt > 0 && kt + 1 < t.ktiles) issue(kt + 1, (kt + 1) & 1);
         }
@@ -574,22 +616,33 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
     if (wp * 64 < t.cols) {
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int m0 = (WQ + 2 * a) * 32;
+        const int m0 = (WQ + NW * a) * 32;
         if (m0 < t.rows) store_block<OP, 2>(P, t, lds + 2 * SB + w * 4096, acc[a], m0, wp * 64, 0, lane);
       }
     }
     if (!more) break;
-    full = t.rows == 256 && t.cols == 256;
+    full = t.rows == TM && t.cols == 256;
     t = next;
   }
+}
+
+// Workgroup b's place in the tile order: consecutive places on one XCD
+// (workgroups are dealt to the 8 XCDs in turn).
+__device__ __forceinline__ int place(int b, int G) { return G % 8 == 0 ? (b % 8) * (G / 8) + b / 8 : b; }
+
+// The weight gradients of experts with few rows.
+template <int OP>
+__global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * 12 * 64 * 32 + 4 * 4096];
+  if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
+  weight_tiles_body<OP, 4, true, 0>(P, (lds_t*)smem, place(blockIdx.x, gridDim.x), gridDim.x);
 }
 
 template <int OP>
 __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kGemmLds];
   lds_t* lds = (lds_t*)smem;
-  const int G = gridDim.x, b = blockIdx.x;
-  const int lid = (G % 8 == 0) ? (b % 8) * (G / 8) + b / 8 : b;  // consecutive ids on one XCD
+  const int G = gridDim.x, lid = place(blockIdx.x, G);
   // rejected row indices or offsets: nothing is computed
   if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
   if constexpr (OP <= BWD_DX) {
@@ -618,11 +671,11 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
   } else {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (w >= 8 - kLoaders) {
-      if (w & 1) weight_tiles_body<OP, true, 1>(P, lds, lid, G);
-      else weight_tiles_body<OP, true, 0>(P, lds, lid, G);
+      if (w & 1) weight_tiles_body<OP, 8, true, 1>(P, lds, lid, G);
+      else weight_tiles_body<OP, 8, true, 0>(P, lds, lid, G);
     } else {
-      if (w & 1) weight_tiles_body<OP, false, 1>(P, lds, lid, G);
-      else weight_tiles_body<OP, false, 0>(P, lds, lid, G);
+      if (w & 1) weight_tiles_body<OP, 8, false, 1>(P, lds, lid, G);
+      else weight_tiles_body<OP, 8, false, 0>(P, lds, lid, G);
     }
   }
 }
@@ -678,11 +731,22 @@ hipError_t launch_expert_backward(const moe_problem_t& p, const Layout& L, char*
     hipLaunchKernelGGL(kern, dim3(G), dim3(kBwdThreads), 0, s, P);
     e = hipGetLastError();
   };
+  auto go2 = [&](auto kern) {
+    if (e != hipSuccess) return;
+    hipLaunchKernelGGL(kern, dim3(2 * G), dim3(256), 0, s, P);
+    e = hipGetLastError();
+  };
   go(expert_backward_kernel<BWD_GU>);
   go(expert_backward_kernel<BWD_DACT>);
   go(expert_backward_kernel<BWD_DX>);
-  go(expert_backward_kernel<BWD_DW2>);
-  go(expert_backward_kernel<BWD_DW1>);
+  // rows per expert, if the router spreads them evenly
+  if ((int64_t)p.T * p.k <= (int64_t)kShortRows * p.E_global) {
+    go2(weight_backward_short_kernel<BWD_DW2>);
+    go2(weight_backward_short_kernel<BWD_DW1>);
+  } else {
+    go(expert_backward_kernel<BWD_DW2>);
+    go(expert_backward_kernel<BWD_DW1>);
+  }
   return e;
 }
 
