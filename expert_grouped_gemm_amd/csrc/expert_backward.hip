@@ -576,17 +576,14 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
       if (t.ktiles > 1) issue(1, 1);
     }
   };
-  if (lid >= total) return;
-  BwdTile t = tile_at(lid);
-  start(t, false);
-  bool full = false;
-  for (int64_t i = lid;;) {
+  for (int64_t i = lid; i < total; i += G) {
+    const BwdTile t = tile_at(i);
+    start(t, false);
     f32x16 acc[4][2];
     clear_acc(acc);
     for (int kt = 0; kt < t.ktiles; ++kt) {
       if constexpr (LOADER) {
         if (kt == 0 && t.ktiles > 1) wait_vmcnt<LD>();
-        else if (kt < 2 && full) wait_vmcnt<16>();
         else wait_vmcnt<0>();
       }
       lds_barrier();
@@ -606,13 +603,6 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
       });
     }
     lds_barrier();  // the ring is free
-    i += G;
-    const bool more = i < total;
-    BwdTile next;
-    if (more) {
-      next = tile_at(i);
-      start(next, next.e == t.e);
-    }
     if (wp * 64 < t.cols) {
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
@@ -620,9 +610,6 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
         if (m0 < t.rows) store_block<OP, 2>(P, t, lds + 2 * SB + w * 4096, acc[a], m0, wp * 64, 0, lane);
       }
     }
-    if (!more) break;
-    full = t.rows == TM && t.cols == 256;
-    t = next;
   }
 }
 
