@@ -180,24 +180,24 @@ struct BandLoads {
 };
 
 // An expert's rows as K (KS), BK of them a stage, perhaps through idx. Lane kk
-// keeps the offset of K row kk of the stage for all lanes; rows past the last
-// re-read it (the stage's LDS rows are zeroed). With idx, the first two stages'
-// rows are kept while the expert stays, so that the next tile's first loads
-// wait for no index; later stages' are fetched when the stage before is issued.
-// Offsets through idx fit 32 bits (the problem limits keep T * d and cap * d
-// below 2^31 elements); without, they count from the stage's first row.
-template <int BLOCKS, int BK>
+// holds the offset of K row kk of a stage for all lanes; rows past the last
+// re-read it (the stage's LDS rows are zeroed). Offsets through idx fit 32 bits
+// (the problem limits keep T * d and cap * d below 2^31 elements) and are
+// fetched ahead: those of a tile's first S stages together, a later stage's
+// when the stage before it is issued. Without idx they count from the stage's
+// first row.
+template <int BLOCKS, int BK, int S>
 struct RowLoads {
   static constexpr int CPR = BLOCKS * 4, RPI = 64 / CPR, NI = BK * BLOCKS / 64;
   const uint8_t* base;
-  uint32_t pitch, lane_off, r0, r1, next;
+  uint32_t pitch, lane_off, ahead[S];
   const int32_t* idx;
   int div, valid;
 
   __device__ __forceinline__ uint32_t look_up(int kt, int lane) const {
     return (uint32_t)(idx[min(kt * BK + (lane & (BK - 1)), valid - 1)] / div) * pitch;
   }
-  __device__ __forceinline__ void init(const Side& s, int lw, int lane, bool same_expert) {
+  __device__ __forceinline__ void init(const Side& s, int lw, int lane) {
     base = s.base;
     pitch = s.pitch;
     idx = s.idx;
@@ -205,12 +205,12 @@ struct RowLoads {
     valid = s.valid;
     const int kk = lw * RPI + lane / CPR;
     lane_off = (((lane % CPR) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
-    if (idx && !same_expert && valid > 0) {
-      r0 = look_up(0, lane);
-      r1 = look_up(1, lane);
+    if (idx && valid > 0) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) ahead[i] = look_up(i, lane);
     }
   }
-  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
+  __device__ __forceinline__ void issue_rows(int kt, uint32_t rows, lds_t* st, int lw, int lane) {
     const int kk = lw * RPI + lane / CPR, left = valid - kt * BK;
     const uint8_t* b0 = idx ? base : base + (size_t)kt * BK * pitch;
     if (!idx && left >= BK) {
@@ -220,11 +220,21 @@ struct RowLoads {
         dma16<false>(b0 + (size_t)(4 * j * RPI) * pitch, off, st + (4 * j + lw) * 1024);
       return;
     }
-    const uint32_t rows = !idx ? min(lane & (BK - 1), left - 1) * pitch : kt == 0 ? r0 : kt == 1 ? r1 : next;
-    if (idx && kt > 0 && left > BK) next = look_up(kt + 1, lane);
+    if (!idx) rows = min(lane & (BK - 1), left - 1) * pitch;
 #pragma unroll
     for (int j = 0; j < NI; ++j)
       dma16<false>(b0, (uint32_t)__shfl((int)rows, 4 * j * RPI + kk, 64) + lane_off, st + (4 * j + lw) * 1024);
+  }
+  // stage kt < S, of the tile's first ones
+  __device__ __forceinline__ void issue_first(int kt, lds_t* st, int lw, int lane) {
+    issue_rows(kt, ahead[kt], st, lw, lane);
+    if (kt == S - 1 && idx) ahead[0] = look_up(S, lane);
+  }
+  // a later stage
+  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
+    const uint32_t rows = ahead[0];
+    if (idx && (kt + 1) * BK < valid) ahead[0] = look_up(kt + 1, lane);
+    issue_rows(kt, rows, st, lw, lane);
   }
 };
 
@@ -516,7 +526,6 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
   t.rows = min(TM, M - t.row0);
   t.col0 = n * 256;
   t.cols = min(256, N - t.col0);
-  t.ktiles = TM == 256 ? (cnt + 63) / 64 : (cnt + 31) / 32;
   const uint32_t db = (uint32_t)P.d * 2, fb = (uint32_t)P.f * 2;
   if constexpr (OP == BWD_DW2) {
     t.P = Side{reinterpret_cast<const uint8_t*>(P.act) + (size_t)r0 * fb + (size_t)t.col0 * 2, fb, cnt, t.cols / 8,
@@ -531,63 +540,52 @@ __device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m,
   return t;
 }
 
-// DW1 or DW2: a workgroup's tiles, one after the other. A tile's first two
-// stages are loaded while its predecessor's results are still being stored,
-// which go through LDS of their own (4 KiB per wavefront behind the two-stage
-// ring).
-// WAVES = 8: 256 x 256 tiles, 64 K rows a stage, one workgroup per CU, the
-// last four wavefronts load. WAVES = 4: 128 x 256 tiles, 32 K rows a stage, two
-// workgroups per CU (72 KiB of LDS each), every wavefront loads: for experts
-// of few rows, whose tiles are a few stages long and otherwise stores, setup and
-// waits, which the two workgroups overlap.
-// The loader's wait for stage kt: vmcnt counts loads and stores in order; the
-// LD or more loads of stage 1 stand behind stage 0, and behind stage 1 the 16
-// stores per wavefront of a full predecessor (`full`).
+// DW1 or DW2: a workgroup's tiles, one after the other.
+// WAVES = 8: 256 x 256 tiles, a ring of two stages of 64 K rows, one workgroup
+// per CU, the last four wavefronts load. WAVES = 4: 128 x 256 tiles, three
+// stages of 32 K rows, two workgroups per CU (72 KiB of LDS each), every
+// wavefront loads: for experts of few rows, whose tiles are a few stages long
+// and otherwise setup, waits and stores, which the two workgroups overlap.
+// A tile starts with the whole ring in flight; from step 1 on, each step
+// refills the slot of the step before it.
 template <int OP, int WAVES, bool LOADER, int WQ>
 __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds, int lid, int G) {
-  constexpr int QB = WAVES, BK = WAVES == 8 ? 64 : 32, NW = WAVES / 4, TM = QB * 32;
+  constexpr int QB = WAVES, BK = WAVES == 8 ? 64 : 32, S = WAVES == 8 ? 2 : 3, NW = WAVES / 4, TM = QB * 32;
   constexpr int SB = (8 + QB) * 64 * BK;  // stage bytes: 64 of each block per K row
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w / NW, lw = w - (WAVES - 4);
-  const int M = (OP == BWD_DW2 ? P.d : 2 * P.f) / TM + ((OP == BWD_DW2 ? P.d : 2 * P.f) % TM != 0);
-  const int N = ((OP == BWD_DW2 ? P.f : P.d) + 255) / 256;
+  const int rows_all = OP == BWD_DW2 ? P.d : 2 * P.f, cols_all = OP == BWD_DW2 ? P.f : P.d;
+  const int M = (rows_all + TM - 1) / TM, N = (cols_all + 255) / 256;
   const int64_t total = (int64_t)P.El * M * N;
-  auto tile_at = [&](int64_t i) {
+  typedef RowLoads<8, BK, S> LoadsP;
+  typedef RowLoads<QB, BK, S> LoadsQ;
+  constexpr int LD = LoadsP::NI + LoadsQ::NI;
+  for (int64_t i = lid; i < total; i += G) {
     const int e = (int)(i / (M * N));
     int m, n;
     raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
-    return weight_tile<OP>(P, e, m, n, TM);
-  };
-  typedef RowLoads<8, BK> LoadsP;
-  typedef RowLoads<QB, BK> LoadsQ;
-  constexpr int LD = LoadsP::NI + LoadsQ::NI;
-  LoadsP lp;
-  LoadsQ lq;
-  auto issue = [&](int kt, int slot) {
-    lp.issue(kt, lds + slot * SB, lw, lane);
-    lq.issue(kt, lds + slot * SB + 8 * 64 * BK, lw, lane);
-  };
-  auto start = [&](const BwdTile& t, bool same_expert) {
+    const BwdTile t = weight_tile<OP>(P, e, m, n, TM);
+    const int KT = (t.P.valid + BK - 1) / BK;
+    LoadsP lp;
+    LoadsQ lq;
     if constexpr (LOADER) {
-      lp.init(t.P, lw, lane, same_expert);
-      lq.init(t.Q, lw, lane, same_expert);
-      if (t.ktiles > 0) issue(0, 0);
-      if (t.ktiles > 1) issue(1, 1);
+      lp.init(t.P, lw, lane);
+      lq.init(t.Q, lw, lane);
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s < KT) {
+          lp.issue_first(s, lds + s * SB, lw, lane);
+          lq.issue_first(s, lds + s * SB + 8 * 64 * BK, lw, lane);
+        }
     }
-  };
-  for (int64_t i = lid; i < total; i += G) {
-    const BwdTile t = tile_at(i);
-    start(t, false);
     f32x16 acc[4][2];
     clear_acc(acc);
-    for (int kt = 0; kt < t.ktiles; ++kt) {
-      if constexpr (LOADER) {
-        if (kt == 0 && t.ktiles > 1) wait_vmcnt<LD>();
-        else wait_vmcnt<0>();
-      }
+    int rd = 0, wr = S - 1;
+    for (int kt = 0; kt < KT; ++kt) {
+      if constexpr (LOADER) wait_stages<LD, S - 1>(min(KT - 1, kt == 0 ? S - 1 : kt + S - 2) - kt);
       lds_barrier();
-      lds_t* st = lds + (kt & 1) * SB;
+      lds_t* st = lds + rd * SB;
       // K rows past the expert's last: zero on both sides
       const int left = t.P.valid - kt * BK;
       if (left < BK) {
@@ -598,18 +596,24 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
       }
       bwd_stage<true, true, 8, QB, 4, BK, NW>(st, WQ, wp, lane, acc, [&]() {
         if constexpr (LOADER) {
-          if (kt > 0 && kt + 1 < t.ktiles) issue(kt + 1, (kt + 1) & 1);
+          if (kt > 0 && kt + S - 1 < KT) {
+            lp.issue(kt + S - 1, lds + wr * SB, lw, lane);
+            lq.issue(kt + S - 1, lds + wr * SB + 8 * 64 * BK, lw, lane);
+          }
         }
       });
+      rd = rd + 1 == S ? 0 : rd + 1;
+      wr = wr + 1 == S ? 0 : wr + 1;
     }
     lds_barrier();  // the ring is free
     if (wp * 64 < t.cols) {
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         const int m0 = (WQ + NW * a) * 32;
-        if (m0 < t.rows) store_block<OP, 2>(P, t, lds + 2 * SB + w * 4096, acc[a], m0, wp * 64, 0, lane);
+        if (m0 < t.rows) store_block<OP, 2>(P, t, lds + w * 4096, acc[a], m0, wp * 64, 0, lane);
       }
     }
+    lds_barrier();  // ... for the next tile's loads
   }
 }
 
@@ -620,7 +624,7 @@ __device__ __forceinline__ int place(int b, int G) { return G % 8 == 0 ? (b % 8)
 // The weight gradients of experts with few rows.
 template <int OP>
 __global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * 12 * 64 * 32 + 4 * 4096];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * 12 * 64 * 32];
   if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
   weight_tiles_body<OP, 4, true, 0>(P, (lds_t*)smem, place(blockIdx.x, gridDim.x), gridDim.x);
 }
