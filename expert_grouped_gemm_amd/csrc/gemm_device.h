@@ -257,7 +257,7 @@ __host__ __device__ constexpr int stage_b_rows_per_round(int OT) {
 }
 __host__ __device__ constexpr int stage_loads(int MB, int NNB, int OT) {
   return (MB * 32 + stage_a_rows_per_round(OT) - 1) / stage_a_rows_per_round(OT) +
-         NNB * 64 / stage_b_rows_per_round(OT) + (OT == OT_W4A4 ? 2 + NNB / 2 : OT ? 2 : 0);
+         NNB * 64 / stage_b_rows_per_round(OT) + (OT == OT_W4A4 ? (MB + 3) / 4 + NNB / 2 : OT ? 2 : 0);
 }
 
 // Wavefront grid of a tile of width NNB: WM wavefront rows x WN wavefront
@@ -357,16 +357,17 @@ __device__ __forceinline__ void issue_load(const Tile& t, int kt, lds_t* st, int
     const uint8_t* g = base + (uint32_t)((r & (half - 1)) * (uint32_t)t.ldb + kt * KBB + (chunk << 4));
     __builtin_amdgcn_global_load_lds(g, st + stage_a_bytes(MB, OT) + r0 * KBB, 16, 0, NT ? kCpolNT : 0);
   } else if constexpr (OT == OT_W4A4) {
-    // E8M0 scales, 8 bytes per row as two dwords in consecutive lanes: two
-    // instructions for the 256 band rows, then NNB / 2 for the weight rows
+    // E8M0 scales, 8 bytes per row as two dwords in consecutive lanes: one or
+    // two instructions for the band rows, then NNB / 2 for the weight rows
+    constexpr int NSA = (MB + 3) / 4;
     lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     const int js = j - NA - NBW;
     const uint32_t dw = kt == t.khalf ? 0 : lane & 1;  // the half slice has one dword
-    if (js < 2) {
+    if (js < NSA) {
       const uint8_t* g = t.Ae + (t.srow[js] + (uint32_t)(kt * 8 + dw * 4));
       __builtin_amdgcn_global_load_lds(g, ss + (js * NW + w) * 256, 4, 0, 0);
     } else {
-      const int r0 = ((js - 2) * NW + w) * 32, r = r0 + (lane >> 1);
+      const int r0 = ((js - NSA) * NW + w) * 32, r = r0 + (lane >> 1);
       const uint8_t* base = r0 < half ? t.Eg : t.Eu;
       const uint8_t* g = base + (uint32_t)((r & (half - 1)) * (uint32_t)t.epitch + kt * 8 + dw * 4);
       __builtin_amdgcn_global_load_lds(g, ss + kBM * 8 + r0 * 8, 4, 0, 0);
@@ -424,7 +425,7 @@ __device__ __forceinline__ void fill_arow(Tile& t, int tid) {
   }
   if constexpr (OT == OT_W4A4) {
 #pragma unroll
-    for (int js = 0; js < 2; ++js) {
+    for (int js = 0; js < (MB + 3) / 4; ++js) {
       const int r = (js * NW + w) * 32 + ((tid & 63) >> 1);
       const int gr = r < t.rows ? r : t.rows - 1;
       t.srow[js] = (uint32_t)(t.a_src ? t.a_src[t.row0 + gr] / t.a_k : gr) * (uint32_t)t.epitch;
@@ -642,7 +643,9 @@ __device__ __forceinline__ void compute_stage_w4(const lds_t* sa, const lds_t* s
 // and no partial sums as in the e4m3 stages). A row's eight scale bytes are
 // two dwords; shifted by 8 h, bytes 0 and 2 of a dword are the lane's scales
 // of two consecutive steps, which the instruction selects by itself.
-// Transposed accumulators as in the other stages. LAST: the stage may be the
+// Transposed accumulators as in the other stages. (Fragments read one K step
+// ahead with a loader's loads behind the first, as in the bf16 stage, made
+// Linear-1 of 16384 rows 1240 -> 1380 us.) LAST: the stage may be the
 // half slice (the K extent ends after its first 128 values), which kslice
 // puts last: only there does a branch stand between the MFMAs. (With the
 // choice in every stage the compiler kept two sets of accumulators and

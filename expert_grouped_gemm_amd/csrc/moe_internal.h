@@ -187,6 +187,7 @@ struct BackwardLayout {
   size_t gu;    // fp32 [cap, 2f]  gate and up
   size_t act;   // bf16 [cap, f]   SwiGLU output
   size_t dh;    // bf16 [cap, 2f]  gradients of gate and up
+  size_t x_rows, do_rows;  // bf16 [cap, d] copies in expert order, where experts have many rows
   size_t total;
 };
 BackwardLayout backward_layout(const moe_problem_t& p, const Layout& L);
