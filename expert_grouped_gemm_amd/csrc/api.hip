@@ -58,6 +58,10 @@ moe_status_t check_ws(const moe::Layout& L, const void* ws, size_t bytes) {
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
 
+// The experts' gradient addresses the 256 rows of a tile by 32-bit offsets (of
+// rows up to 4 f bytes).
+bool backward_widths_ok(const moe_problem_t& p) { return p.d <= 1 << 20 && p.f <= 1 << 20; }
+
 // Shapes of the MXFP4 codec: whole blocks, and an element count that 64-bit
 // byte offsets hold with room to spare.
 moe_status_t check_mxfp4_shape(int64_t rows, int64_t cols) {
@@ -390,7 +394,7 @@ MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY
 }
 
 MOE_API size_t moe_backward_workspace_size(const moe_problem_t* p) {
-  if (check_problem(p) != MOE_OK || p->dtype != MOE_DTYPE_BF16) return 0;
+  if (check_problem(p) != MOE_OK || p->dtype != MOE_DTYPE_BF16 || !backward_widths_ok(*p)) return 0;
   return moe::backward_layout(*p, moe::make_layout(*p)).total;
 }
 
@@ -401,6 +405,7 @@ MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, 
   moe_status_t st = check_problem(p);
   if (st != MOE_OK) return st;
   if (p->dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!backward_widths_ok(*p)) return MOE_ERR_UNSUPPORTED;
   if (!X || !offsets || !row_dst || !W1 || !W2 || !d_combine_buf || !d_x_slots || !dW1 || !dW2)
     return MOE_ERR_INVALID_ARGUMENT;
   for (const void* q : {X, W1, W2, d_combine_buf, (const void*)d_x_slots, (const void*)dW1, (const void*)dW2})

@@ -468,7 +468,7 @@ MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d
  * forward) and the gradients of gate and up are rounded to bf16, being
  * operands of products; sums are fp32 and each output is rounded once. The
  * same call gives the same bits.
- * bf16 only (MOE_ERR_UNSUPPORTED otherwise). The workspace is one of
+ * bf16 only, d and f at most 2^20 (MOE_ERR_UNSUPPORTED otherwise). The workspace is one of
  * moe_backward_workspace_size(p) bytes (0 for an invalid or non-bf16
  * problem): a workspace of moe_workspace_size(p) with this call's
  * intermediates behind it, so it serves the forward calls too; of their

@@ -254,7 +254,8 @@ def test_expert_backward_arguments_rejected_before_launch(L):
             args[i] = f[j]
             assert L.moe_expert_backward(P, *args, need, None) == 1, (i, j)
     assert L.moe_expert_backward(P, *f, ctypes.c_size_t(need.value - 1), None) == 3
-    for dtype in ("fp8_e4m3", "w4a8_mxfp4"):
-        q = moe.make_problem(128, 128, 256, 4, 2, dtype=dtype)
+    for q in (moe.make_problem(128, 128, 256, 4, 2, dtype="fp8_e4m3"),
+              moe.make_problem(128, 128, 256, 4, 2, dtype="w4a8_mxfp4"),
+              moe.make_problem(1, 128, (1 << 20) + 128, 1, 1), moe.make_problem(1, (1 << 20) + 128, 128, 1, 1)):
         assert L.moe_backward_workspace_size(ctypes.byref(q)) == 0
         assert L.moe_expert_backward(ctypes.byref(q), *f, need, None) == 2

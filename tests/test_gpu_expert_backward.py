@@ -172,6 +172,46 @@ def test_rows_per_expert_around_the_tile_borders(counts):
     _check((dxs[dst], dW1, dW2), backward.expert_backward(*ops), _rounded_reference(*ops), _bounds(*ops), counts)
 
 
+def test_rows_that_do_not_start_at_zero():
+    """offsets[0] > 0: the rows before it belong to no expert."""
+    A, d, f, first = 90, 128, 128, 7
+    off = np.array([first, 40, 40, A])
+    g = torch.Generator().manual_seed(8)
+    p = moe.make_problem(A, d, f, 3, 1, sched="auto")
+    X, dO = (torch.randn(A, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    W1, W2 = (torch.randn(*s, generator=g).mul_(0.05).to(torch.bfloat16) for s in ((3, 2 * f, d), (3, d, f)))
+    X[:first] = float("nan")
+    z = dict(dtype=torch.bfloat16, device="cuda")
+    out = torch.full((A, d), 3.0, **z), torch.empty(3, 2 * f, d, **z), torch.empty(3, d, f, **z)
+    ws = moe.alloc_backward_workspace(p)
+    moe.expert_backward(p, X.cuda(), None, _i32(off), _i32(np.arange(A)), W1.cuda(), W2.cuda(), dO.cuda(), *out, ws)
+    torch.cuda.synchronize()
+    moe.check_workspace(p, ws)
+    dxs, dW1, dW2 = (t.double().cpu().numpy() for t in out)
+    assert np.all(dxs[:first] == 3.0)
+    ops = (X.double().numpy()[first:], dO.double().numpy()[first:], off - first, W1.double().numpy(),
+           W2.double().numpy())
+    _check((dxs[first:], dW1, dW2), backward.expert_backward(*ops), _rounded_reference(*ops), _bounds(*ops), "first")
+
+
+@pytest.mark.parametrize("T", [300, 1300])
+def test_on_another_stream(T):
+    """Both weight-gradient forms on a stream of the caller's, against the default stream."""
+    cfg, inp, disp, dO = _setup(dict(T=T, d=256, f=128, E_global=2, k=1))
+    p = problem_of(cfg, sched="auto")
+    args = (inp["X"].cuda(), _i32(disp["row_src"], cfg.cap), _i32(disp["offsets"]), _i32(disp["row_dst"], cfg.cap),
+            inp["W1"].cuda(), inp["W2"].cuda(), dO.cuda())
+    a, b = _outputs(cfg), _outputs(cfg)
+    ws, ws2 = moe.alloc_backward_workspace(p), moe.alloc_backward_workspace(p)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    moe.expert_backward(p, *args, *a, ws, stream=side)
+    moe.expert_backward(p, *args, *b, ws2)
+    torch.cuda.synchronize()
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
 def test_saturated_gates():
     """Gates far out on both sides: the derivative is 0 or 1 there, never NaN."""
     T, d, f = 40, 128, 128
