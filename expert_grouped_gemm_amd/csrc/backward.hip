@@ -48,9 +48,10 @@ __device__ __forceinline__ float wave_sum(float x) {
 
 constexpr int kMaxK = 16;
 
-// One workgroup per token. The slots are taken two at a time: dY's row is
-// read once per pair, and the pair's dots are summed over the workgroup at
-// the end.
+// One workgroup per token, slot by slot (dY's row, read again for each, is in the
+// caches by then); the dots are summed over the workgroup at the end. Bound by
+// HBM: on the share (4096 tokens, 4100 slots, d = 7168, 256 logits) 53 us for 239
+// MB, 4.5 TB/s where a large copy reaches 5.2.
 template <bool BF16_IN>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const uint16_t* __restrict__ dY, const void* __restrict__ buf, const int32_t* __restrict__ tok_off,
@@ -117,8 +118,75 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
   }
 }
 
+// Rows of at most 1024 columns: one wavefront per token, in which groups of GS
+// lanes take a slot each (a row of 128 columns is 16 lanes' 8 columns: four
+// slots at once). With a workgroup per token, 14817 tokens of d = 128, k = 5 took
+// 41 us, this 13.
+template <bool BF16_IN, int GS>
+__global__ __launch_bounds__(256) void combine_backward_narrow_kernel(
+    const uint16_t* __restrict__ dY, const void* __restrict__ buf, const int32_t* __restrict__ tok_off,
+    const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, int T, int d, int k, int E, int e_begin,
+    int El, int S, int cap, uint16_t* __restrict__ dO, float* __restrict__ d_w, float* __restrict__ d_logits) {
+  __shared__ float s_dw[4][kMaxK];
+  __shared__ int s_gate[4][kMaxK];  // gate of the token's n-th slot
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, t = blockIdx.x * 4 + wv;
+  if (t >= T) return;  // whole wavefronts; nothing below waits for another one
+  const int q = y_row_of_token(t, T, S);
+  const int idx = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
+  const float w = lane < k ? topk_w[(size_t)t * k + lane] : 0.0f;
+  const bool local = lane < k && (unsigned)(idx - e_begin) < (unsigned)El;
+  const uint64_t mask = __ballot(local);
+  const int p0 = tok_off[q], p1 = tok_off[q + 1], cnt = __popcll(mask);
+  const bool ok = 0 <= p0 && p1 <= cap && p1 - p0 == cnt;  // as above
+  if (lane < kMaxK) s_dw[wv][lane] = 0.0f;
+  if (local) s_gate[wv][__popcll(mask & ((1ull << lane) - 1ull))] = lane;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  if (ok) {
+    const int vec = d >> 3, g = lane / GS, c0 = lane % GS;
+    const uint4* dy_row = reinterpret_cast<const uint4*>(dY + (size_t)q * d);
+    for (int n = g; n < cnt; n += 64 / GS) {
+      const int j = s_gate[wv][n], p = p0 + n;
+      const float wj = topk_w[(size_t)t * k + j];  // (the groups' loops differ in length: no shuffle here)
+      float acc = 0.0f;
+      for (int c = c0; c < vec; c += GS) {
+        float dy[8], o[8];
+        unpack8(dy_row[c], dy);
+        combine_load8<BF16_IN>(buf, (size_t)p, d, c, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc = fmaf(dy[i], o[i], acc);
+          dy[i] *= wj;
+        }
+        reinterpret_cast<uint4*>(dO + (size_t)p * d)[c] = pack8(dy);
+      }
+#pragma unroll
+      for (int off = GS / 2; off > 0; off >>= 1) acc += __shfl_xor(acc, off, GS);
+      if (c0 == 0) s_dw[wv][j] = acc;
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  float dw = lane < k ? s_dw[wv][lane] : 0.0f;
+  if (!ok) dw = __builtin_nanf("");
+  const float mean = wave_sum(lane < k ? w * dw : 0.0f);
+  const float dl = w * (dw - mean);
+  if (lane < k) d_w[(size_t)t * k + lane] = dw;
+  if (!d_logits) return;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    float v = ok ? 0.0f : __builtin_nanf("");
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl(idx, j, 64);
+      const float dj = __shfl(dl, j, 64);
+      if (ej == e) v += dj;
+    }
+    if (e < E) d_logits[(size_t)t * E + e] = v;
+  }
+}
+
 // dX[t] = the sum of the token's slots, ascending, in fp32, rounded once.
-// Streaming: one thread per 8 columns of a token.
+// Streaming: one thread per 8 columns of a token. Bound by HBM: on the share 25 us
+// for 117 MB, 4.7 TB/s; 32768 tokens with four slots of d = 2048 120 us for 671
+// MB (5.6 TB/s, part of it out of the last-level cache).
 __global__ __launch_bounds__(256) void dispatch_backward_kernel(const uint16_t* __restrict__ dxs,
                                                                 const int32_t* __restrict__ tok_off, int T, int d,
                                                                 int S, int cap, uint16_t* __restrict__ dX,
@@ -154,13 +222,26 @@ __global__ __launch_bounds__(256) void dispatch_backward_kernel(const uint16_t* 
 hipError_t launch_combine_backward(const moe_problem_t& p, const void* dY, const void* combine_buf,
                                    const int32_t* tok_off, const int32_t* topk_idx, const float* topk_w, void* dO,
                                    float* d_w, float* d_logits, hipStream_t s) {
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(p.T), dim3(256), 0, s, static_cast<const uint16_t*>(dY), combine_buf, tok_off,
+  auto go = [&](auto kern, int blocks) {
+    hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, s, static_cast<const uint16_t*>(dY), combine_buf, tok_off,
                        topk_idx, topk_w, p.T, p.d, p.k, p.E_global, p.e_begin, p.e_end - p.e_begin, p.num_segments,
                        (int)row_capacity(p), static_cast<uint16_t*>(dO), d_w, d_logits);
   };
-  if (p.flags & MOE_FLAG_BF16_COMBINE_BUF) go(combine_backward_kernel<true>);
-  else go(combine_backward_kernel<false>);
+  const bool bf16 = (p.flags & MOE_FLAG_BF16_COMBINE_BUF) != 0;
+  const int four = (p.T + 3) / 4;
+  if (p.d > 1024) {
+    if (bf16) go(combine_backward_kernel<true>, p.T);
+    else go(combine_backward_kernel<false>, p.T);
+  } else if (p.d > 256) {
+    if (bf16) go(combine_backward_narrow_kernel<true, 64>, four);
+    else go(combine_backward_narrow_kernel<false, 64>, four);
+  } else if (p.d > 128) {
+    if (bf16) go(combine_backward_narrow_kernel<true, 32>, four);
+    else go(combine_backward_narrow_kernel<false, 32>, four);
+  } else {
+    if (bf16) go(combine_backward_narrow_kernel<true, 16>, four);
+    else go(combine_backward_narrow_kernel<false, 16>, four);
+  }
   return hipGetLastError();
 }
 

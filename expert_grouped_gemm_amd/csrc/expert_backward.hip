@@ -22,6 +22,19 @@
 // with the tile's 256 columns each and is read by the transposing LDS read
 // (ds_read_b64_tr_b16: 16 lanes take 4 K rows x 16 columns, lane i ends with
 // the 4 K values of column i), so no operand is ever transposed in memory.
+//
+// Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
+// without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
+// but for the weight gradients, whose tiles of two to five stages are half setup
+// and stores: GU 372 (5.0 TB/s), DACT 200 (4.7), DX 400 (4.7), DW2 334 (2.8), DW1 656
+// (2.9). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the step's loads,
+// LDS reads and MFMAs, which overlap to about 1.8 us a stage where the MFMAs alone
+// take 1.0 at the clock the chip holds: GU 3565 (1079), DACT 2281 (844, with the
+// epilogue's 3.3 GB), DX 3492 (1102), DW2 1829 (1052), DW1 3687 (1044).
+// Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
+// fragments read across the barrier (20% slower), every wavefront loading (6%),
+// the next weight-gradient tile's loads issued before the stores of the last
+// (its registers spilled).
 #include "gemm_device.h"
 
 namespace moe {
@@ -518,6 +531,15 @@ __device__ __forceinline__ BwdTile band_tile(const BwdParams& P, int p, int n, i
   return t;
 }
 
+// Rows [first, first + count) of a band's tile.
+__device__ __forceinline__ void take_rows(BwdTile& t, int first, int count) {
+  t.rows = min(count, t.rows - first);
+  t.row0 += first;
+  t.Q.valid = t.rows;
+  if (t.Q.idx) t.Q.idx += first;
+  else t.Q.base += (size_t)first * t.Q.pitch;
+}
+
 // Tile (m, n) of an expert's weight gradient, TM rows high. IDX: the rows of X
 // and dO are looked up; otherwise they are read from their ordered copies.
 template <int OP, bool IDX>
@@ -665,14 +687,20 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
     const int nb = P.meta[META_P];
     const int width = OP == BWD_GU ? 2 * P.f : OP == BWD_DACT ? P.f : P.d;
     const int N = (width + 255) / 256, total = nb * N, cut = total / G * G;
-    // whole rounds of 256-column tiles, then the rest as halves
-    for (int i = lid; i < cut + 2 * (total - cut); i += G) {
+    // Whole rounds of 256-column tiles, then the rest as halves. Where even the
+    // halves leave workgroups idle, they are cut along the band's rows too, in
+    // two or four: a smaller stage takes less time and makes a deeper ring (one
+    // expert of 274 rows, d = 3584, f = 1024: 175 -> 125 us).
+    int cuts = 1;
+    while (cuts < 4 && 4 * cuts * (total - cut) <= G) cuts *= 2;
+    for (int i = lid; i < cut + 2 * cuts * (total - cut); i += G) {
       const bool wide = i < cut;
       int p, n;
-      raster(wide ? i : cut + ((i - cut) >> 1), nb, N, P.group_m, p, n);
+      raster(wide ? i : cut + (i - cut) / (2 * cuts), nb, N, P.group_m, p, n);
       if (!wide) n = 2 * n + ((i - cut) & 1);
-      const BwdTile t = band_tile<OP>(P, p, n, wide ? 256 : 128);
-      if (t.cols <= 0) continue;
+      BwdTile t = band_tile<OP>(P, p, n, wide ? 256 : 128);
+      if (!wide) take_rows(t, (((i - cut) >> 1) & (cuts - 1)) * (kBM / cuts), kBM / cuts);
+      if (t.cols <= 0 || t.rows <= 0) continue;
       // weights of an expert with one band are read once per launch (see
       // streams_once)
       const bool once = (P.band_expert[p] & kBandSingle) != 0;

@@ -30,6 +30,9 @@ CASES = {
     "segments": dict(T=96, d=640, E_global=8, k=3, e_begin=0, e_end=5, num_segments=4),
     "wide_rows": dict(T=33, d=7168, E_global=256, k=8, e_begin=0, e_end=32),
     "none_local": dict(T=5, d=128, E_global=512, k=2, e_begin=511, e_end=512),
+    "rows_of_1024": dict(T=37, d=1024, E_global=12, k=5),
+    "rows_past_1024": dict(T=19, d=1152, E_global=12, k=5, e_begin=2, e_end=9),
+    "rows_of_256": dict(T=43, d=256, E_global=16, k=7, e_begin=0, e_end=9),
     "many_experts": dict(T=20, d=128, E_global=1024, k=8),
 }
 

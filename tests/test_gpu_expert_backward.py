@@ -41,6 +41,7 @@ CASES = {
     "none_local": dict(T=2, d=128, f=128, E_global=512, k=1, e_begin=511, e_end=512),
     "long_experts": dict(T=1500, d=384, f=640, E_global=2, k=1),
     "long_many_tiles": dict(T=1111, d=2304, f=1152, E_global=4, k=2),
+    "one_expert": dict(T=274, d=896, f=384, E_global=1, k=1),
     "many_tiles": dict(T=900, d=1536, f=2048, E_global=3, k=1),
 }
 
