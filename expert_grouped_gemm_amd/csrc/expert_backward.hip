@@ -26,11 +26,11 @@
 // Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
 // without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
 // but for the weight gradients, whose tiles of two to five stages are half setup
-// and stores: GU 372 (5.0 TB/s), DACT 200 (4.7), DX 400 (4.7), DW2 334 (2.8), DW1 656
-// (2.9). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the step's loads,
-// LDS reads and MFMAs, which overlap to about 1.8 us a stage where the MFMAs alone
-// take 1.0 at the clock the chip holds: GU 3565 (1079), DACT 2281 (844, with the
-// epilogue's 3.3 GB), DX 3492 (1102), DW2 1829 (1052), DW1 3687 (1044).
+// and stores: GU 361 (5.2 TB/s), DACT 187 (5.0), DX 387 (4.9), DW2 292 (3.2), DW1 600
+// (3.1). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy
+// 59% of the time at the clock the chip holds under them, and the loads and LDS
+// reads that do not overlap with them: GU 3544 (1086), DACT 2288 (841, with the
+// epilogue's 3.3 GB), DX 3466 (1110), DW2 1822 (1056), DW1 3658 (1052).
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
 // fragments read across the barrier (20% slower), every wavefront loading (6%),
 // the next weight-gradient tile's loads issued before the stores of the last
