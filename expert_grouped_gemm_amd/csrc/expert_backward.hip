@@ -116,7 +116,9 @@ __device__ __forceinline__ int ks_swizzle(int kk) { return (kk & 3) << 2; }
 // the loaders then stood still in every stage until the next stage's data had
 // come, and the ring overlapped nothing. The load has no register result; its
 // completion is waited for in wait_vmcnt() before the barrier that publishes
-// the stage.
+// the stage. The wait states between are the instruction's own to keep: one
+// after the write of M0, and five after a vector instruction (readfirstlane)
+// that wrote the scalar base.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // M0 is reserved, and named as overwritten
 template <bool NT>
@@ -126,10 +128,10 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, lds_t* 
                       ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32);
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)st);
   if constexpr (NT)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(m0), "v"(off), "s"(sb)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(m0), "v"(off), "s"(sb)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(sb)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(sb)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop

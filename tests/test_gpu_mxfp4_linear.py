@@ -27,7 +27,7 @@ CASES = {
     "half_slices": dict(T=70, d=384, f=128, E_global=8, k=2, e_begin=1, e_end=6),
     "odd_rows": dict(T=333, d=256, f=640, E_global=16, k=4, e_begin=0, e_end=8),
     "bands": dict(T=700, d=512, f=384, E_global=2, k=1),
-    "full_bands_long_k": dict(T=600, d=2048, f=1536, E_global=1, k=1),
+    "full_bands_long_k": dict(T=600, d=2048, f=1664, E_global=1, k=1),
     "many_tiles": dict(T=1200, d=1024, f=6400, E_global=4, k=2),
     "long_k": dict(T=40, d=7168, f=256, E_global=64, k=8, e_begin=0, e_end=8),
     "empty_experts": dict(T=3, d=640, f=256, E_global=256, k=2, e_begin=0, e_end=128),
