@@ -781,7 +781,7 @@ hipError_t launch_expert_backward(const moe_problem_t& p, const Layout& L, char*
   P.d = p.d;
   P.f = p.f;
   P.El = L.E_l;
-  P.group_m = 4;
+  P.group_m = 4;  // as in the forward (2: GU and DW1 of long experts 4% slower; 8: DW2 2%)
   auto go = [&](auto kern) {
     if (e != hipSuccess) return;
     hipLaunchKernelGGL(kern, dim3(G), dim3(kBwdThreads), 0, s, P);
