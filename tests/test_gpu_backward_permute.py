@@ -81,6 +81,9 @@ def test_combine_backward(name, bf16_buf):
     tol_l = np.zeros_like(r_l)
     np.put_along_axis(tol_l, idx.astype(np.int64), tol, axis=1)
     assert np.all(np.abs(d_l.double().cpu().numpy() - r_l) <= tol_l)
+    d_w2 = torch.empty_like(d_w)                 # without the logits' gradient
+    moe.combine_backward(p, dY.cuda(), buf.cuda(), _i32(disp["tok_off"]), _i32(idx), w.cuda(), d_buf, d_w2)
+    assert torch.equal(d_w, d_w2)
 
 
 @pytest.mark.parametrize("name", list(CASES))

@@ -213,6 +213,21 @@ def test_on_another_stream(T):
         assert torch.equal(x, y)
 
 
+def test_grid_changes_no_bit():
+    cfg, inp, disp, dO = _setup(CASES["odd_widths"])
+    args = (inp["X"].cuda(), _i32(disp["row_src"], cfg.cap), _i32(disp["offsets"]), _i32(disp["row_dst"], cfg.cap),
+            inp["W1"].cuda(), inp["W2"].cuda(), dO.cuda())
+    ref = None
+    for grid in (0, 1, 2, 7, 40):
+        p = problem_of(cfg, sched="auto", grid=grid)
+        out = _outputs(cfg)
+        moe.expert_backward(p, *args, *out, moe.alloc_backward_workspace(p))
+        torch.cuda.synchronize()
+        ref = ref or out
+        for a, b in zip(ref, out):
+            assert torch.equal(a, b), grid
+
+
 def test_saturated_gates():
     """Gates far out on both sides: the derivative is 0 or 1 there, never NaN."""
     T, d, f = 40, 128, 128

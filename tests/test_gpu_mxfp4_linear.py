@@ -251,6 +251,20 @@ def test_rows_past_the_last_are_not_looked_at():
     moe.check_workspace(p, ws)
 
 
+def test_grid_and_raster_change_no_bit():
+    cfg, disp, g = _setup(CASES["half_slices"])
+    (x, xs), (w, ws_) = _rand_mx(g, cfg.T, cfg.d), _rand_mx(g, cfg.E_local, 2 * cfg.f, cfg.d)
+    ref = None
+    for kw in (dict(), dict(grid=1), dict(grid=2), dict(grid=9), dict(tiles="narrow"), dict(band_major=True)):
+        p = problem_of(cfg, sched="auto", **kw)
+        H = torch.zeros(cfg.cap, cfg.f, dtype=torch.bfloat16, device="cuda")
+        moe.mxfp4_linear1(p, x.cuda(), xs.cuda(), _i32(disp["row_src"], cfg.cap), _i32(disp["offsets"]), w.cuda(),
+                          ws_.cuda(), H, moe.alloc_workspace(p))
+        torch.cuda.synchronize()
+        ref = H if ref is None else ref
+        assert torch.equal(ref, H), kw
+
+
 def test_replayed_graph():
     cfg, disp, g = _setup(CASES["odd_rows"])
     p = problem_of(cfg, sched="auto")
