@@ -32,9 +32,10 @@
 // reads that do not overlap with them: GU 3544 (1086), DACT 2288 (841, with the
 // epilogue's 3.3 GB), DX 3466 (1110), DW2 1822 (1056), DW1 3658 (1052).
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
-// fragments read across the barrier (20% slower), every wavefront loading (6%),
-// the next weight-gradient tile's loads issued before the stores of the last
-// (its registers spilled).
+// fragments read across the barrier (20% slower) and every wavefront loading
+// (6%), both while the loads still went through the builtin (see dma16); the
+// next weight-gradient tile's loads issued before the stores of the last, and
+// DACT's gate and up values all fetched ahead of its stores (registers spilled).
 #include "gemm_device.h"
 
 namespace moe {
