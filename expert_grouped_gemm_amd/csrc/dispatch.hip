@@ -35,6 +35,7 @@ __global__ __launch_bounds__(256) void dispatch_count_kernel(const int32_t* __re
   if (blockIdx.x == 0 && threadIdx.x == 0) {  // the error words report this call only
     meta[META_ERR] = 0;
     meta[META_ARG_ERR] = 0;
+    meta[META_TAG] = kMetaTag;
   }
   extern __shared__ int32_t hist_all[];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;

@@ -658,7 +658,7 @@ __device__ __forceinline__ int place(int b, int G) { return G % 8 == 0 ? (b % 8)
 // stage cost DW1 of 16384 rows 13% (4280 against 3780 us), the copies take 120
 // us. 16 bytes per lane.
 __global__ __launch_bounds__(256) void order_rows_kernel(BwdParams P) {
-  if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
+  if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
   const int first = P.offsets[0], last = P.offsets[P.El], vec = P.d >> 3;
   const int64_t n = (int64_t)(last - first) * vec;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -675,7 +675,7 @@ __global__ __launch_bounds__(256) void order_rows_kernel(BwdParams P) {
 template <int OP>
 __global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * 12 * 64 * 32];
-  if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
+  if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
   weight_tiles_body<OP, 4, true, 0>(P, (lds_t*)smem, place(blockIdx.x, gridDim.x), gridDim.x);
 }
 
@@ -685,7 +685,7 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
   lds_t* lds = (lds_t*)smem;
   const int G = gridDim.x, lid = place(blockIdx.x, G);
   // rejected row indices or offsets: nothing is computed
-  if (P.meta[META_ARG_ERR] & ARG_ERR_ALL) return;
+  if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
   if constexpr (OP <= BWD_DX) {
     const int nb = P.meta[META_P];
     const int width = OP == BWD_GU ? 2 * P.f : OP == BWD_DACT ? P.f : P.d;
@@ -754,7 +754,7 @@ hipError_t launch_expert_backward(const moe_problem_t& p, const Layout& L, char*
                                   hipStream_t s) {
   const int G = gemm_grid(p);
   if (G <= 0) return hipErrorInvalidDevice;
-  hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, s);
+  hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP | ARG_ERR_LINEAR1, 0, s);
   if (e != hipSuccess) return e;
   const BackwardLayout B = backward_layout(p, L);
   auto I = [&](size_t off) { return reinterpret_cast<const int32_t*>(ws + off); };

@@ -27,11 +27,12 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
 // row_src entries outside [0, src_end) or row_dst entries outside [0, cap),
 // among the rows the offsets cover, empty the plan as well (no tile runs,
 // nothing is read through them) and set their error bits. Either array may be
-// null. One block: the whole of plan_body plus these checks took 12 us on the
+// null. What earlier calls on the workspace reported stays: a timed-out wait,
+// and the bits `keep` of the argument errors. One block: the whole of plan_body plus these checks took 12 us on the
 // share (4096 rows, 32 experts), this takes 5.
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap,
                                                          const int32_t* __restrict__ row_src, int64_t src_end,
-                                                         const int32_t* __restrict__ row_dst,
+                                                         const int32_t* __restrict__ row_dst, int keep, int mark,
                                                          int32_t* __restrict__ band_expert,
                                                          int32_t* __restrict__ band_row0,
                                                          int32_t* __restrict__ band_rows, int32_t* __restrict__ meta) {
@@ -41,6 +42,8 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
   __shared__ int err;
   const int e = threadIdx.x, lane = e & 63, wv = e >> 6, waves = blockDim.x >> 6;
   if (e == 0) err = 0;
+  const bool written = meta[META_TAG] == kMetaTag;
+  const int wait_err = written ? meta[META_ERR] : 0, kept = written ? meta[META_ARG_ERR] & keep : 0;
   const int lo = e < El ? offsets[e] : 0, hi = e < El ? offsets[e + 1] : 0;
   const int first = offsets[0], last = offsets[El];
   __syncthreads();
@@ -82,9 +85,10 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
   }
   __syncthreads();
   if (e == 0) {
-    meta[META_ERR] = 0;
+    meta[META_ERR] = wait_err;
     meta[META_TRACE_N] = 0;
-    meta[META_ARG_ERR] = err;
+    meta[META_ARG_ERR] = kept | err | (err ? mark : 0);
+    meta[META_TAG] = kMetaTag;
   }
   if (err) {
     if (e == 0) meta[META_P] = meta[META_A] = 0;
@@ -129,12 +133,12 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
 }  // namespace
 
 hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
-                            const int32_t* row_src, const int32_t* row_dst, hipStream_t s) {
+                            const int32_t* row_src, const int32_t* row_dst, int keep, int mark, hipStream_t s) {
   auto I = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   // a thread per expert at least; enough of them for the row indices
   const int threads = L.E_l > 256 || L.cap > 65536 ? 1024 : 256;
   hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(threads), 0, s, offsets, L.E_l, L.cap, row_src, (int64_t)p.T * p.k,
-                     row_dst, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.pub.meta));
+                     row_dst, keep, mark, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.pub.meta));
   return hipGetLastError();
 }
 
@@ -306,7 +310,9 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
                                hipStream_t s) {
   const int G = gemm_grid(p);
   if (G <= 0) return hipErrorInvalidDevice;
-  const hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, s);
+  const hipError_t e =
+      first ? launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP, ARG_ERR_LINEAR1, s)
+            : launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP | ARG_ERR_LINEAR1, 0, s);
   if (e != hipSuccess) return e;
   GemmParams P = gemm_params(p, L, ws, G, A, nullptr, row_dst, W, nullptr, W, nullptr, out, nullptr, 0);
   P.Xe = P.He = A_scale;

@@ -27,15 +27,24 @@ enum MetaSlot {
   META_A = 0, META_P = 1, META_ERR = 2, META_NWAVES = 3, META_TRACE_N = 4, META_ARG_ERR = 5,
   // moe_layer_forward's fused dispatch kernel: the scan-done flag, cleared by
   // the router kernel that starts each call
-  META_SCAN_DONE = 6
+  META_SCAN_DONE = 6,
+  // kMetaTag once a call has written the error words: without it they are what
+  // the memory held before its first use as a workspace
+  META_TAG = 7
 };
+constexpr int kMetaTag = 0x4D6F4531;
 // Bits of meta[META_ARG_ERR]: device-side checks of arguments the host cannot
-// see (they live in device memory). A call that uses a workspace clears the
-// whole word when it starts (the workspace may hold anything before its first
-// use); inside moe_layer_forward the expert GEMM clears only its own bits, so
-// the dispatch's report survives until moe_check_workspace reads it.
+// see (they live in device memory). A call that starts a layer clears the
+// whole word (the workspace may hold anything before its first use); inside
+// moe_layer_forward the expert GEMM clears only its own bits, so the
+// dispatch's report survives until moe_check_workspace reads it. The calls that
+// follow others on the same arrays (the MXFP4 Linears, the experts' gradient)
+// clear the bits of their own checks, ARG_ERR_PLAN, and leave what the calls
+// before them reported: the dispatch, a forward's timed-out wait, and
+// ARG_ERR_LINEAR1, that Linear-1 was rejected and left H as it was.
 enum ArgErr {
-  ARG_ERR_DISPATCH_CAP = 1, ARG_ERR_OFFSETS = 2, ARG_ERR_ROW_DST = 4, ARG_ERR_ROW_SRC = 8, ARG_ERR_ALL = 15
+  ARG_ERR_DISPATCH_CAP = 1, ARG_ERR_OFFSETS = 2, ARG_ERR_ROW_DST = 4, ARG_ERR_ROW_SRC = 8, ARG_ERR_LINEAR1 = 16,
+  ARG_ERR_PLAN = 14, ARG_ERR_ALL = 31
 };
 
 // band_expert[p] of the band table: the band's local expert, plus
@@ -178,9 +187,11 @@ hipError_t launch_expert_forward_fused(const moe_problem_t& p, const Layout& L, 
                                        void* combine_buf, hipStream_t s);
 
 // The row-band plan of a call with its own offsets, row_src and row_dst
-// (either of the last two may be null), its row indices checked.
+// (either of the last two may be null), its row indices checked. keep: the bits
+// of meta[META_ARG_ERR] it leaves as earlier calls set them; mark: a bit it
+// adds to a rejection.
 hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, const int32_t* offsets,
-                            const int32_t* row_src, const int32_t* row_dst, hipStream_t s);
+                            const int32_t* row_src, const int32_t* row_dst, int keep, int mark, hipStream_t s);
 
 // moe_expert_backward's intermediates, behind the workspace's own regions.
 struct BackwardLayout {

@@ -28,6 +28,7 @@ __device__ __forceinline__ void plan_body(const int32_t* __restrict__ offsets, i
   for (int i = threadIdx.x; i < nblk_done; i += blockDim.x) blk_done[i] = 0;
   if (threadIdx.x == 0) {
     meta[META_ERR] = 0;  // the flag reports this call only
+    meta[META_TAG] = kMetaTag;
     meta[META_TRACE_N] = 0;
     __hip_atomic_fetch_and(meta + META_ARG_ERR, ~clear_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }

@@ -134,6 +134,7 @@ __global__ __launch_bounds__(512) void route_count_kernel(const float* __restric
   if (b == 0 && threadIdx.x == 0) {
     meta[META_ERR] = 0;
     meta[META_ARG_ERR] = 0;
+    meta[META_TAG] = kMetaTag;
     meta[META_SCAN_DONE] = 0;
   }
   for (int e = threadIdx.x; e < El; e += blockDim.x) hist[e] = 0;

@@ -195,7 +195,8 @@ typedef struct moe_workspace_layout {
                                             errors (bits: 1 = more local assignments than the row
                                             capacity, 2 = offsets not monotone or past the row
                                             capacity, 4 = a row_dst outside the row capacity,
-                                            8 = a row_src outside [0, T*k)) */
+                                            8 = a row_src outside [0, T*k), 16 = moe_mxfp4_linear1
+                                            rejected its offsets or row_src) */
   size_t tile_trace;    /* moe_tile_record_t [tile_trace_capacity]; empty without MOE_FLAG_TILE_TRACE */
   size_t tile_trace_capacity;  /* records (a bound on the tiles of one call) */
   size_t total;         /* = moe_workspace_size */
@@ -306,7 +307,11 @@ MOE_API moe_status_t moe_layer_forward(const moe_problem_t* p, const void* X, co
  * MOE_ERR_DEADLOCK if a persistent-pipeline wait of the most recent
  * expert-GEMM call on this workspace timed out, MOE_ERR_INVALID_ARGUMENT if a
  * device-side check of the last dispatch or expert-GEMM call failed (its
- * outputs are then invalid). Clears both words. */
+ * outputs are then invalid). moe_mxfp4_linear1, moe_mxfp4_linear2 and
+ * moe_expert_backward follow other calls of a layer and leave their reports
+ * (of the dispatch, of a forward that timed out, and in Linear-2 that of
+ * Linear-1): one check after the last call covers them all. Clears both
+ * words. */
 MOE_API moe_status_t moe_check_workspace(const moe_problem_t* p, void* workspace, size_t ws_bytes,
                                          void* stream);
 
