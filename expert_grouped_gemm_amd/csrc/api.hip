@@ -3,6 +3,8 @@
 // dispatch -> grouped expert GEMM -> combine) on the caller's stream.
 #include <string.h>
 
+#include <initializer_list>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -57,6 +59,32 @@ moe_status_t check_ws(const moe::Layout& L, const void* ws, size_t bytes) {
 }
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
+
+// An array of a call. A null one shares bytes with nothing.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+// Whether an output shares bytes with an input or with another output: the
+// kernels read and write their arrays in no order that would allow it.
+bool shares_bytes(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span* q = o + 1; q != outputs.end(); ++q)
+      if (meet(*o, *q)) return true;
+    for (const Span& i : inputs)
+      if (meet(*o, i)) return true;
+  }
+  return false;
+}
+
+// The error words, counts and band tables at the start of a workspace (the
+// arrays behind them may be a call's operands).
+Span workspace_tables(const moe::Layout& L, const void* ws) { return {ws, L.pub.topk_idx}; }
 
 // The experts' gradient addresses the 256 rows of a tile by 32-bit offsets (of
 // rows up to 4 f bytes).
@@ -387,7 +415,14 @@ MOE_API moe_status_t moe_combine_backward(const moe_problem_t* p, const void* dY
   if (!dY || !combine_buf || !tok_off || !topk_idx || !topk_w || !d_combine_buf || !d_topk_w)
     return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned16(dY) || !aligned16(combine_buf) || !aligned16(d_combine_buf)) return MOE_ERR_INVALID_ARGUMENT;
-  if (combine_buf == d_combine_buf) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t slots = (size_t)moe::row_capacity(*p) * p->d, gates = (size_t)p->T * p->k * 4;
+  if (shares_bytes({{d_combine_buf, slots * 2}, {d_topk_w, gates}, {d_logits, (size_t)p->T * p->E_global * 4}},
+                   {{dY, (size_t)p->T * p->d * 2},
+                    {combine_buf, slots * (p->flags & MOE_FLAG_BF16_COMBINE_BUF ? 2 : 4)},
+                    {tok_off, ((size_t)p->T + 1) * 4},
+                    {topk_idx, gates},
+                    {topk_w, gates}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_combine_backward(*p, dY, combine_buf, tok_off, topk_idx, topk_w, d_combine_buf,
                                                     d_topk_w, d_logits, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
@@ -410,12 +445,21 @@ MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, 
     return MOE_ERR_INVALID_ARGUMENT;
   for (const void* q : {X, W1, W2, d_combine_buf, (const void*)d_x_slots, (const void*)dW1, (const void*)dW2})
     if (!aligned16(q)) return MOE_ERR_INVALID_ARGUMENT;
-  // the inputs are read until the last launch
-  for (const void* in : {X, W1, W2, d_combine_buf})
-    if (in == d_x_slots || in == dW1 || in == dW2) return MOE_ERR_INVALID_ARGUMENT;
   const moe::Layout L = moe::make_layout(*p);
+  const size_t slots = (size_t)L.cap * p->d * 2, w = (size_t)L.E_l * p->d * p->f * 2;
+  const Span in_X{X, row_src ? (size_t)p->T * p->d * 2 : slots}, in_src{row_src, (size_t)L.cap * 4},
+      in_off{offsets, ((size_t)L.E_l + 1) * 4}, in_dst{row_dst, (size_t)L.cap * 4}, in_W1{W1, 2 * w}, in_W2{W2, w},
+      in_dO{d_combine_buf, slots};
+  if (shares_bytes({{d_x_slots, slots}, {dW1, 2 * w}, {dW2, w}}, {in_X, in_src, in_off, in_dst, in_W1, in_W2, in_dO}))
+    return MOE_ERR_INVALID_ARGUMENT;
   if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
-  if (ws_bytes < moe::backward_layout(*p, L).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const moe::BackwardLayout B = moe::backward_layout(*p, L);
+  if (ws_bytes < B.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  // the tables and intermediates this call writes in the workspace
+  const Span tables = workspace_tables(L, workspace), inner{static_cast<char*>(workspace) + B.gu, B.total - B.gu};
+  if (shares_bytes({tables, inner}, {in_X, in_src, in_off, in_dst, in_W1, in_W2, in_dO, {d_x_slots, slots},
+                                     {dW1, 2 * w}, {dW2, w}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_expert_backward(*p, L, static_cast<char*>(workspace), X, row_src, offsets, row_dst,
                                                    W1, W2, d_combine_buf, d_x_slots, dW1, dW2, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
@@ -425,8 +469,12 @@ MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d
                                            void* dX, float* dX_fp32, void* stream) {
   moe_status_t st = check_problem(p);
   if (st != MOE_OK) return st;
-  if (!d_x_slots || !tok_off || !dX || d_x_slots == dX) return MOE_ERR_INVALID_ARGUMENT;
+  if (!d_x_slots || !tok_off || !dX) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned16(d_x_slots) || !aligned16(dX) || (dX_fp32 && !aligned16(dX_fp32))) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)p->T * p->d;
+  if (shares_bytes({{dX, n * 2}, {dX_fp32, n * 4}},
+                   {{d_x_slots, (size_t)moe::row_capacity(*p) * p->d * 2}, {tok_off, ((size_t)p->T + 1) * 4}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_dispatch_backward(*p, d_x_slots, tok_off, dX, dX_fp32, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
@@ -442,6 +490,15 @@ MOE_API moe_status_t moe_mxfp4_linear1(const moe_problem_t* p, const uint8_t* X,
     return MOE_ERR_INVALID_ARGUMENT;
   const moe::Layout L = moe::make_layout(*p);
   if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const size_t rows = row_src ? (size_t)p->T : (size_t)L.cap, w = (size_t)L.E_l * 2 * p->f * p->d;
+  const Span out{H, (size_t)L.cap * p->f * 2}, tables = workspace_tables(L, workspace);
+  if (shares_bytes({out, tables}, {{X, rows * p->d / 2},
+                                   {X_scale, rows * p->d / 32},
+                                   {row_src, (size_t)L.cap * 4},
+                                   {offsets, ((size_t)L.E_l + 1) * 4},
+                                   {W1, w / 2},
+                                   {W1_scale, w / 32}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_mxfp4_linear(*p, L, static_cast<char*>(workspace), true, X, X_scale, row_src,
                                                 offsets, nullptr, W1, W1_scale, H, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
@@ -458,6 +515,16 @@ MOE_API moe_status_t moe_mxfp4_linear2(const moe_problem_t* p, const uint8_t* H,
     return MOE_ERR_INVALID_ARGUMENT;
   const moe::Layout L = moe::make_layout(*p);
   if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const size_t h = (size_t)L.cap * p->f, w = (size_t)L.E_l * p->d * p->f;
+  const Span out{combine_buf, (size_t)L.cap * p->d * (p->flags & MOE_FLAG_BF16_COMBINE_BUF ? 2 : 4)},
+      tables = workspace_tables(L, workspace);
+  if (shares_bytes({out, tables}, {{H, h / 2},
+                                   {H_scale, h / 32},
+                                   {offsets, ((size_t)L.E_l + 1) * 4},
+                                   {row_dst, (size_t)L.cap * 4},
+                                   {W2, w / 2},
+                                   {W2_scale, w / 32}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_mxfp4_linear(*p, L, static_cast<char*>(workspace), false, H, H_scale, nullptr,
                                                 offsets, row_dst, W2, W2_scale, combine_buf, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
@@ -469,6 +536,8 @@ MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows,
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{codes, n / 2}, {scales, n / 32}}, {{x, n * (x_fp32 ? 4 : 2)}})) return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_mxfp4_quantize(x, x_fp32 != 0, rows * cols, codes, scales, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
@@ -479,6 +548,9 @@ MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* s
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{out, n * (out_fp32 ? 4 : 2)}}, {{codes, n / 2}, {scales, n / 32}}))
+    return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_mxfp4_dequantize(codes, scales, rows * cols, out, out_fp32 != 0,
                                                     (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);

@@ -423,6 +423,11 @@ MOE_API moe_status_t moe_segment_copy_wait(const moe_problem_t* p, const float* 
 /* Gradients of the layer's two permutations, for a training step. Both work
  * on any operand type of p (they touch none of the experts' operands).
  *
+ * For these two, moe_expert_backward and the MXFP4 calls below, an output that
+ * shares bytes with an input or with another output (or, where there is a
+ * workspace, with the parts of it that the call writes) is
+ * MOE_ERR_INVALID_ARGUMENT.
+ *
  * moe_combine_backward: the gradient of moe_combine with moe_route_topk's
  * softmax behind it. dY bf16 [T, d] in output-row order q; combine_buf [cap,
  * d] as moe_combine read it (fp32, or bf16 with MOE_FLAG_BF16_COMBINE_BUF);
@@ -477,8 +482,7 @@ MOE_API moe_status_t moe_dispatch_backward(const moe_problem_t* p, const void* d
  * moe_backward_workspace_size(p) bytes (0 for an invalid or non-bf16
  * problem): a workspace of moe_workspace_size(p) with this call's
  * intermediates behind it, so it serves the forward calls too; of their
- * regions this call writes only meta and the row-band tables. Inputs may not be
- * outputs. Device-side checks as in moe_mxfp4_linear1 (offsets, row_src,
+ * regions this call writes only meta and the row-band tables. Device-side checks as in moe_mxfp4_linear1 (offsets, row_src,
  * row_dst): if one fails no output is written. */
 MOE_API size_t moe_backward_workspace_size(const moe_problem_t* p);
 MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, const int32_t* row_src,
@@ -489,7 +493,7 @@ MOE_API moe_status_t moe_expert_backward(const moe_problem_t* p, const void* X, 
 /* MXFP4 codec (OCP MXFP4: E2M1 elements, two per byte, the even element in
  * the low nibble; one E8M0 scale byte per 32 consecutive elements of a row).
  * x [rows, cols], cols % 32 == 0, rows >= 0, DEVICE memory; codes uint8
- * [rows, cols/2], scales uint8 [rows, cols/32]. codes 16-byte aligned.
+ * [rows, cols/2], scales uint8 [rows, cols/32]. x, out and codes 16-byte aligned.
  *
  * moe_mxfp4_quantize (x fp32 if x_fp32, else bf16): per block, scale =
  * 2^(floor(log2 amax) - 2), at least 2^-127 (byte 0; byte 127 for a block of
