@@ -144,9 +144,9 @@ __device__ __forceinline__ void dma16(const uint8_t* base, uint32_t off, lds_t* 
 // to the next, and the swizzle, which depends on the row modulo 16 or 4, stays:
 // an address is a uniform base plus one 32-bit lane offset.
 
-// A weight matrix: every row exists, at its own place. Of a 256-column tile
-// only 128 columns may exist: the others re-read those. NT: with the
-// non-temporal hint.
+// A weight matrix: every row exists, at its own place. Of a KS tile of 256
+// columns only 128 may exist: the others re-read those (the rows of a KC tile
+// all exist: 2f is a multiple of 256). NT: with the non-temporal hint.
 template <bool KS, int BLOCKS, bool NT>
 struct WeightLoads {
   static constexpr int NI = BLOCKS;                       // BLOCKS * 4 KiB over 4 loaders
@@ -154,12 +154,10 @@ struct WeightLoads {
   static constexpr int RPI = 64 / CPR;                    // rows per instruction
   const uint8_t* base;
   uint32_t pitch, lane_off;
-  int valid;
 
   __device__ __forceinline__ void init(const Side& s, int lw, int lane) {
     base = s.base;
     pitch = s.pitch;
-    valid = s.valid;
     const int r = lw * RPI + lane / CPR, c = lane % CPR;
     if constexpr (KS) lane_off = r * pitch + (((c ^ ks_swizzle(r)) & (s.chunks - 1)) << 4);
     else lane_off = r * pitch + ((c ^ chunk_swizzle<128>(r)) << 4);
@@ -167,10 +165,8 @@ struct WeightLoads {
   __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int) {
     const uint8_t* b0 = base + (KS ? (size_t)kt * kBK * pitch : (size_t)kt * (kBK * 2));
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int step = KS || j * 4 * RPI < valid ? j : j - NI / 2;
-      dma16<NT>(b0 + (size_t)step * (4 * RPI) * pitch, lane_off, st + (4 * j + lw) * 1024);
-    }
+    for (int j = 0; j < NI; ++j)
+      dma16<NT>(b0 + (size_t)(j * 4 * RPI) * pitch, lane_off, st + (4 * j + lw) * 1024);
   }
 };
 
