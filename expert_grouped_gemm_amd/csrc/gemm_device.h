@@ -647,9 +647,12 @@ __device__ __forceinline__ void compute_stage_w4(const lds_t* sa, const lds_t* s
 // ahead with a loader's loads behind the first, as in the bf16 stage, made
 // Linear-1 of 16384 rows 1240 -> 1380 us.) LAST: the stage may be the
 // half slice (the K extent ends after its first 128 values), which kslice
-// puts last: only there does a branch stand between the MFMAs. (With the
-// choice in every stage the compiler kept two sets of accumulators and
-// spilled.)
+// puts last: only there does a branch stand between the MFMAs. With the choice
+// in every stage the compiler kept two sets of accumulators, copied from one to
+// the other by products whose result began inside their own addend (the
+// instruction takes the two in the same registers or in disjoint ones, and for
+// the scaled one the compiler did not see to it): those elements lost products.
+// tests/test_mfma_operands.py reads the built code for such a product.
 template <int NMB, int NNB, bool LAST>
 __device__ __forceinline__ void compute_stage_w4a4(const lds_t* sa, const lds_t* sb, const lds_t* ss, int tid,
                                                    bool half_slice,
