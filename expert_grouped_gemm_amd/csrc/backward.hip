@@ -120,8 +120,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
 
 // Rows of at most 1024 columns: one wavefront per token, in which groups of GS
 // lanes take a slot each (a row of 128 columns is 16 lanes' 8 columns: four
-// slots at once). With a workgroup per token, 14817 tokens of d = 128, k = 5 took
-// 41 us, this 13.
+// slots at once). Against a workgroup per token, us: 14817 tokens of d = 128, k = 5
+// 41 -> 13; 16384 tokens, k = 6, d = 512 77 -> 59, 768 95 -> 95, 1024 119 -> 127,
+// 1280 152 -> 171; 2048 tokens, 512 10.7 -> 8.7, 1024 14.7 -> 14.3, 2048 26.6 -> 27.5; 64
+// tokens the same up to 1536, then slower (3584: 8.3 -> 13.5).
 template <bool BF16_IN, int GS>
 __global__ __launch_bounds__(256) void combine_backward_narrow_kernel(
     const uint16_t* __restrict__ dY, const void* __restrict__ buf, const int32_t* __restrict__ tok_off,

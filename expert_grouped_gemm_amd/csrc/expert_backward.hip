@@ -26,11 +26,14 @@
 // Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
 // without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
 // but for the weight gradients, whose tiles of two to five stages are half setup
-// and stores: GU 361 (5.2 TB/s), DACT 187 (5.0), DX 387 (4.9), DW2 292 (3.2), DW1 600
-// (3.1). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy
+// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DX 386 (4.9), DW2 291 (3.2), DW1 590
+// (3.2). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy
 // 59% of the time at the clock the chip holds under them, and the loads and LDS
-// reads that do not overlap with them: GU 3544 (1086), DACT 2288 (841, with the
-// epilogue's 3.3 GB), DX 3466 (1110), DW2 1822 (1056), DW1 3658 (1052).
+// reads that do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the
+// epilogue's 3.3 GB), DX 3408 (1129), DW2 1906 (1009), DW1 3751 (1026).
+// These last two (WAVES = 8) spill 16 registers, output row numbers of their
+// epilogue that one loader role reloads between its stores; no accumulator and
+// nothing of a K loop is spilled, and no other kernel here spills any.
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
 // fragments read across the barrier (20% slower) and every wavefront loading
 // (6%), both while the loads still went through the builtin (see dma16); the
@@ -68,7 +71,17 @@ __host__ __device__ constexpr int bwd_ring(int PB, int QB) {
   return s > 6 ? 6 : s;
 }
 
-constexpr int kShortRows = 512;              // rows per expert up to which weight_backward_short_kernel runs
+// Rows per expert up to which weight_backward_short_kernel runs. Whole calls
+// with it / with the other kernel and its copies, us:
+//   rows per expert              128          256          512         1024          2048
+//   32 experts, d 7168, f 2048   1812 / 1932  3340 / 3335  5257 / 5090  9179 / 8623  17264 / 15646
+//   8 of 4096, 14336                          3444 / 3401  5458 / 5182  9294 / 8576  17291 / 15308
+//   16 of 2048, 1024              183 / 203    279 / 295    453 / 458    767 / 763    1402 / 1359
+// They cross between 256 and 640 rows; at 512 the two differ by at most 5%. The
+// rows are the router's mean, T k / E_global, as the host does not see the call's
+// offsets: a share that holds the favoured experts may take the short kernel for
+// long ones (4 of 64 experts, a Zipf router, 8192 tokens: 2119 / 1923).
+constexpr int kShortRows = 512;
 
 struct BwdParams {
   const uint8_t* X;          // token rows [T, d] (through row_src) or expert-ordered rows
@@ -650,9 +663,9 @@ __device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds
 __device__ __forceinline__ int place(int b, int G) { return G % 8 == 0 ? (b % 8) * (G / 8) + b / 8 : b; }
 
 // Copies of the token rows (with row_src) and of the output gradients in expert
-// order, for the weight gradients of long experts: looking the rows up in every
-// stage cost DW1 of 16384 rows 13% (4280 against 3780 us), the copies take 120
-// us. 16 bytes per lane.
+// order, for the weight gradients of long experts: the call of 16384 rows, d =
+// 4096, f = 14336 takes 15.2 ms with the copies (84 us of it) and 16.3 with the
+// rows looked up in every stage. 16 bytes per lane.
 __global__ __launch_bounds__(256) void order_rows_kernel(BwdParams P) {
   if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
   const int first = P.offsets[0], last = P.offsets[P.El], vec = P.d >> 3;
@@ -688,8 +701,11 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
     const int N = (width + 255) / 256, total = nb * N, cut = total / G * G;
     // Whole rounds of 256-column tiles, then the rest as halves. Where even the
     // halves leave workgroups idle, they are cut along the band's rows too, in
-    // two or four: a smaller stage takes less time and makes a deeper ring (one
-    // expert of 274 rows, d = 3584, f = 1024: 175 -> 125 us).
+    // two or four: a smaller stage takes less time and makes a deeper ring. Whole
+    // calls without cuts / with two / with up to four, us: one expert of 274 rows,
+    // d = 3584, f = 1024 180 / 132 / 115; of 128 rows, 2048, 1408 114 / 113 / 103; of
+    // 256 rows, 4096, 4096 331 / 240 / 228; 4 experts of 256 rows, 1024, 512
+    // 114 / 91 / 83.
     int cuts = 1;
     while (cuts < 4 && 4 * cuts * (total - cut) <= G) cuts *= 2;
     for (int i = lid; i < cut + 2 * cuts * (total - cut); i += G) {

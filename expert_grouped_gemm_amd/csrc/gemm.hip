@@ -28,8 +28,9 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
 // among the rows the offsets cover, empty the plan as well (no tile runs,
 // nothing is read through them) and set their error bits. Either array may be
 // null. What earlier calls on the workspace reported stays: a timed-out wait,
-// and the bits `keep` of the argument errors. One block: the whole of plan_body plus these checks took 12 us on the
-// share (4096 rows, 32 experts), this takes 5.
+// and the bits `keep` of the argument errors. One block: the whole of plan_body
+// plus these checks took 12 us on the share (4096 rows, 32 experts), this takes
+// 5 (16384 rows 16, 65536 rows 46: one workgroup reads every index).
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap,
                                                          const int32_t* __restrict__ row_src, int64_t src_end,
                                                          const int32_t* __restrict__ row_dst, int keep, int mark,

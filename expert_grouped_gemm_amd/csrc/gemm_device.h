@@ -238,9 +238,13 @@ __host__ __device__ constexpr int loader_waves(int) { return 4; }
 // us; the counted L2 misses were the same, the hint changed what the misses
 // cost. On experts with several bands (Mixtral, DiT) the hint made every
 // launch slower (4-5%): their weights are read again by the other bands.
-// MXFP4 weight rows are excluded: a stage takes 64 bytes of a row, half a
-// 128-byte line, and the next stage the other half, which a streamed line no
-// longer holds (the W4A8 share's Linear-1 183 -> 191 us with the hint).
+// MXFP4 weight rows against e4m3 rows are excluded: a stage takes 64 bytes of a
+// row, half a 128-byte line, and the next stage the other half, which a streamed
+// line no longer holds (the W4A8 share's Linear-1 183 -> 191 us with the hint).
+// Against MXFP4 rows a stage takes whole lines: the W4A4 share's Linear-1 with
+// 4096 tokens 138 -> 127 us, with 64 103 -> 101, Linear-2 97.5 -> 95. (Only weights
+// that a cache still holds from the call before lose by it: Linear-2 of 64
+// tokens, called over and over on the same 219 MB, 51 -> 55.)
 __host__ __device__ constexpr bool streams_once(int OT) { return stage_kb_bytes(OT) == 128; }
 constexpr int kCpolNT = 2;  // cache-policy operand of the global -> LDS load: nt
 
