@@ -29,6 +29,8 @@ def _weights(g, E, d, f):
     (SINGLE, 384, 640, (2,)), (SEVERAL, 384, 640, (2,)), (SINGLE, 640, 384, (22,)), (SEVERAL, 640, 384, (22, 34)),
     (SEVERAL, 640, 640, (16, 28)),
     ((700, 513, 1100, 900), 640, 384, (2, 8)),     # weight gradients of long experts, several tiles a workgroup
+    ((0, 1600, 1, 1200, 0), 384, 640, (2, 0)),     # ... and of none and one row among them
+    ((1, 0, 2) * 341 + (130,), 128, 128, (0, 6)),  # as many experts as there may be
 ])
 def test_every_tile_form(counts, d, f, grids):
     A, E = sum(counts), len(counts)

@@ -15,11 +15,12 @@ pytestmark = pytest.mark.gpu
 
 COUNTS = {"single": (20, 50, 90, 120, 150, 180, 220, 256), "several": (276, 306, 346, 376, 406, 436, 476, 768),
           "mixed": (0, 600, 5, 0, 257, 1)}
+MOST = (1, 0, 2) * 341 + (130,)     # as many experts as there may be
 GRIDS = (2, 8, 40, 0)
 
 
 def _setup(name, d, f):
-    counts = COUNTS[name]
+    counts = MOST if name == "most" else COUNTS[name]
     A, E = sum(counts), len(counts)
     cfg = moe_synth.make_config("tiny", T=A, d=d, f=f, E_global=E, k=1, e_begin=0, e_end=E)
     rng = np.random.default_rng(A + d + f)
@@ -32,8 +33,8 @@ def _problem(cfg, grid, **kw):
     return moe.make_problem(cfg.T, cfg.d, cfg.f, cfg.E_global, 1, sched="auto", grid=grid, **kw)
 
 
-@pytest.mark.parametrize("d,f", [(1152, 640), (1280, 384)])
-@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("name,d,f", [(n, *s) for n in COUNTS for s in ((1152, 640), (1280, 384))]
+                         + [("most", 128, 256)])
 def test_linear1_tiles(name, d, f):
     cfg, disp, g = _setup(name, d, f)
     (x, xs), (w, ws_) = _rand_mx(g, cfg.T, d), _rand_mx(g, cfg.E_local, 2 * f, d)
@@ -51,8 +52,8 @@ def test_linear1_tiles(name, d, f):
 
 
 @pytest.mark.parametrize("bf16_buf", [False, True])
-@pytest.mark.parametrize("d,f", [(1280, 1152), (768, 1664), (512, 1024)])
-@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("name,d,f", [(n, *s) for n in COUNTS for s in ((1280, 1152), (768, 1664), (512, 1024))]
+                         + [("most", 256, 128)])
 def test_linear2_tiles(name, d, f, bf16_buf):
     cfg, disp, g = _setup(name, d, f)
     A, off, dst = disp["A"], disp["offsets"], disp["row_dst"]
