@@ -22,7 +22,9 @@ __all__ = [
     "check_workspace", "tile_trace", "schedule_of", "store_burst_probe", "owner_plan", "owner_gather",
     "segment_copy", "expert_forward_signal", "segment_copy_wait", "combine_backward", "expert_backward",
     "dispatch_backward", "backward_workspace_size", "alloc_backward_workspace",
-    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear1", "mxfp4_linear2", "SCHED", "DTYPE", "STATUS",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear1", "mxfp4_linear2", "int8_quantize", "int8_dequantize",
+    "int8_linear1", "int8_linear2", "mxint8_quantize", "mxint8_dequantize", "expert_forward_checkpoint",
+    "expert_backward_checkpoint", "checkpoint_workspace_size", "alloc_checkpoint_workspace", "SCHED", "DTYPE", "STATUS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -128,7 +130,18 @@ def lib() -> ctypes.CDLL:
         L.moe_backward_workspace_size.argtypes = [PP]
         L.moe_expert_backward.restype = ctypes.c_int
         L.moe_expert_backward.argtypes = [PP] + [_P] * 11 + [ctypes.c_size_t, _P]
-        for name in ("moe_mxfp4_linear1", "moe_mxfp4_linear2"):
+        for codec in ("int8", "mxint8"):
+            f = getattr(L, f"moe_{codec}_quantize")
+            f.restype, f.argtypes = ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]
+            f = getattr(L, f"moe_{codec}_dequantize")
+            f.restype, f.argtypes = ctypes.c_int, [_P, _P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P]
+        L.moe_expert_forward_checkpoint.restype = ctypes.c_int
+        L.moe_expert_forward_checkpoint.argtypes = [PP] + [_P] * 10 + [ctypes.c_size_t, _P]
+        L.moe_checkpoint_workspace_size.restype = ctypes.c_size_t
+        L.moe_checkpoint_workspace_size.argtypes = [PP]
+        L.moe_expert_backward_checkpoint.restype = ctypes.c_int
+        L.moe_expert_backward_checkpoint.argtypes = [PP] + [_P] * 14 + [ctypes.c_size_t, _P]
+        for name in ("moe_mxfp4_linear1", "moe_mxfp4_linear2", "moe_int8_linear1", "moe_int8_linear2"):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [PP] + [_P] * 8 + [ctypes.c_size_t, _P]
         L.moe_schedule_of.restype = ctypes.c_int
@@ -447,15 +460,15 @@ def dispatch_backward(p: Problem, d_x_slots, tok_off, dX, dX_fp32=None, stream=N
             lambda s: lib().moe_dispatch_backward(ctypes.byref(p), *args, s))
 
 
-def _mxfp4_rows(where: str, name: str, x):
+def _codec_rows(where: str, name: str, x, unit: int = 32):
     """Rows, columns and whether fp32, of the values' tensor of a codec call."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError(f"{where}: {name} must be a tensor of rows")
     if x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
         raise ValueError(f"{where}: {name} is {x.dtype}, expected torch.bfloat16 or torch.float32")
     cols = x.shape[-1]
-    if cols < 1 or cols % 32:
-        raise ValueError(f"{where}: rows of {cols} elements are not whole blocks of 32")
+    if cols < 1 or cols % unit:
+        raise ValueError(f"{where}: rows of {cols} elements are not whole blocks of {unit}")
     return x.numel() // cols, cols, int(x.dtype is torch.float32)
 
 
@@ -464,7 +477,7 @@ def mxfp4_quantize(x, codes, scales, stream=None):
     [..., cols/2] and E8M0 scales uint8 [..., cols/32], blocks along the last
     dimension."""
     w = "mxfp4_quantize"
-    rows, cols, f32 = _mxfp4_rows(w, "x", x)
+    rows, cols, f32 = _codec_rows(w, "x", x)
     n = rows * cols
     px, pc, ps = (_operand(w, "x", x, x.dtype, n), _operand(w, "codes", codes, torch.uint8, n // 2),
                   _operand(w, "scales", scales, torch.uint8, n // 32))
@@ -475,7 +488,7 @@ def mxfp4_dequantize(codes, scales, out, stream=None):
     """moe_mxfp4_dequantize: the values of MXFP4 codes and scales into out
     [..., cols] (bf16 or fp32)."""
     w = "mxfp4_dequantize"
-    rows, cols, f32 = _mxfp4_rows(w, "out", out)
+    rows, cols, f32 = _codec_rows(w, "out", out)
     n = rows * cols
     pc, ps, po = (_operand(w, "codes", codes, torch.uint8, n // 2), _operand(w, "scales", scales, torch.uint8, n // 32),
                   _operand(w, "out", out, out.dtype, n))
@@ -508,6 +521,134 @@ def mxfp4_linear2(p: Problem, H, H_scale, offsets, row_dst, W2, W2_scale, combin
             _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d), _operand(w, "workspace", workspace, u8, 0))
     _launch(w, stream, (H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace),
             lambda s: lib().moe_mxfp4_linear2(ctypes.byref(p), *args, workspace.numel(), s))
+
+
+def int8_quantize(x, codes, scales, stream=None):
+    """moe_int8_quantize: x [..., cols] (bf16 or fp32) into 8-bit integers, codes
+    int8 [..., cols] and scales fp32 [...], one for each row."""
+    w = "int8_quantize"
+    rows, cols, f32 = _codec_rows(w, "x", x, 16)
+    n = rows * cols
+    px, pc, ps = (_operand(w, "x", x, x.dtype, n), _operand(w, "codes", codes, torch.int8, n),
+                  _operand(w, "scales", scales, torch.float32, rows))
+    _launch(w, stream, (x, codes, scales), lambda s: lib().moe_int8_quantize(px, f32, rows, cols, pc, ps, s))
+
+
+def int8_dequantize(codes, scales, out, stream=None):
+    """moe_int8_dequantize: code * scale into out [..., cols] (bf16 or fp32)."""
+    w = "int8_dequantize"
+    rows, cols, f32 = _codec_rows(w, "out", out, 16)
+    n = rows * cols
+    pc, ps, po = (_operand(w, "codes", codes, torch.int8, n), _operand(w, "scales", scales, torch.float32, rows),
+                  _operand(w, "out", out, out.dtype, n))
+    _launch(w, stream, (codes, scales, out), lambda s: lib().moe_int8_dequantize(pc, ps, rows, cols, po, f32, s))
+
+
+def int8_linear1(p: Problem, X, X_scale, row_src, offsets, W1, W1_scale, H, workspace, stream=None):
+    """moe_int8_linear1: the experts' first Linear with SwiGLU on 8-bit integer
+    tokens (gathered through row_src, or already in expert order with
+    row_src=None) and weights, with a scale for each token and each weight row,
+    into H bf16 [cap, f]."""
+    w, i8, f32, cap, El = "int8_linear1", torch.int8, torch.float32, row_capacity(p), p.e_end - p.e_begin
+    rows = cap if row_src is None else p.T
+    args = (_operand(w, "X", X, i8, rows * p.d), _operand(w, "X_scale", X_scale, f32, rows),
+            _operand(w, "row_src", row_src, torch.int32, cap, optional=True),
+            _operand(w, "offsets", offsets, torch.int32, El + 1),
+            _operand(w, "W1", W1, i8, El * 2 * p.f * p.d), _operand(w, "W1_scale", W1_scale, f32, El * 2 * p.f),
+            _operand(w, "H", H, torch.bfloat16, cap * p.f), _operand(w, "workspace", workspace, torch.uint8, 0))
+    _launch(w, stream, (X, X_scale, row_src, offsets, W1, W1_scale, H, workspace),
+            lambda s: lib().moe_int8_linear1(ctypes.byref(p), *args, workspace.numel(), s))
+
+
+def int8_linear2(p: Problem, H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace, stream=None):
+    """moe_int8_linear2: the experts' second Linear on 8-bit integer rows and
+    weights, into the token-order slots of combine_buf."""
+    w, i8, f32, cap, El = "int8_linear2", torch.int8, torch.float32, row_capacity(p), p.e_end - p.e_begin
+    buf_dt = torch.bfloat16 if p.flags & FLAG_BF16_COMBINE_BUF else torch.float32
+    args = (_operand(w, "H", H, i8, cap * p.f), _operand(w, "H_scale", H_scale, f32, cap),
+            _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
+            _operand(w, "W2", W2, i8, El * p.f * p.d), _operand(w, "W2_scale", W2_scale, f32, El * p.d),
+            _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d),
+            _operand(w, "workspace", workspace, torch.uint8, 0))
+    _launch(w, stream, (H, H_scale, offsets, row_dst, W2, W2_scale, combine_buf, workspace),
+            lambda s: lib().moe_int8_linear2(ctypes.byref(p), *args, workspace.numel(), s))
+
+
+def mxint8_quantize(x, codes, scales, stream=None):
+    """moe_mxint8_quantize: x [..., cols] (bf16 or fp32) into MXINT8, codes int8
+    [..., cols] and E8M0 scales uint8 [..., cols/32], blocks along the last
+    dimension."""
+    w = "mxint8_quantize"
+    rows, cols, f32 = _codec_rows(w, "x", x)
+    n = rows * cols
+    px, pc, ps = (_operand(w, "x", x, x.dtype, n), _operand(w, "codes", codes, torch.int8, n),
+                  _operand(w, "scales", scales, torch.uint8, n // 32))
+    _launch(w, stream, (x, codes, scales), lambda s: lib().moe_mxint8_quantize(px, f32, rows, cols, pc, ps, s))
+
+
+def mxint8_dequantize(codes, scales, out, stream=None):
+    """moe_mxint8_dequantize: the values of MXINT8 codes and scales into out
+    [..., cols] (bf16 or fp32)."""
+    w = "mxint8_dequantize"
+    rows, cols, f32 = _codec_rows(w, "out", out)
+    n = rows * cols
+    pc, ps, po = (_operand(w, "codes", codes, torch.int8, n), _operand(w, "scales", scales, torch.uint8, n // 32),
+                  _operand(w, "out", out, out.dtype, n))
+    _launch(w, stream, (codes, scales, out), lambda s: lib().moe_mxint8_dequantize(pc, ps, rows, cols, po, f32, s))
+
+
+def expert_forward_checkpoint(p: Problem, X, row_src, offsets, row_dst, W1, W2, gu, gu_scale, combine_buf, workspace,
+                              stream=None):
+    """moe_expert_forward_checkpoint: the experts' products in bf16 into the slots
+    of combine_buf, leaving the SwiGLU inputs in MXINT8 (gu int8 [cap, 2f],
+    gu_scale uint8 [cap, 2f/32]) for expert_backward_checkpoint. X holds the
+    tokens with row_src, or the rows in expert order with row_src=None."""
+    w, bf, cap, El = "expert_forward_checkpoint", torch.bfloat16, row_capacity(p), p.e_end - p.e_begin
+    buf_dt = bf if p.flags & FLAG_BF16_COMBINE_BUF else torch.float32
+    args = (_operand(w, "X", X, bf, (cap if row_src is None else p.T) * p.d),
+            _operand(w, "row_src", row_src, torch.int32, cap, optional=True),
+            _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
+            _operand(w, "W1", W1, bf, El * 2 * p.f * p.d), _operand(w, "W2", W2, bf, El * p.d * p.f),
+            _operand(w, "gu", gu, torch.int8, cap * 2 * p.f),
+            _operand(w, "gu_scale", gu_scale, torch.uint8, cap * p.f // 16),
+            _operand(w, "combine_buf", combine_buf, buf_dt, cap * p.d),
+            _operand(w, "workspace", workspace, torch.uint8, 0))
+    _launch(w, stream, (X, row_src, offsets, row_dst, W1, W2, gu, gu_scale, combine_buf, workspace),
+            lambda s: lib().moe_expert_forward_checkpoint(ctypes.byref(p), *args, workspace.numel(), s))
+
+
+def checkpoint_workspace_size(p: Problem) -> int:
+    """Bytes of a workspace for expert_backward_checkpoint (which serves the forward calls too)."""
+    n = lib().moe_checkpoint_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise MoEError(2, "moe_checkpoint_workspace_size")
+    return n
+
+
+def alloc_checkpoint_workspace(p: Problem, device="cuda") -> torch.Tensor:
+    return torch.empty(checkpoint_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def expert_backward_checkpoint(p: Problem, X, X_scale, row_src, offsets, row_dst, gu, gu_scale, W1, W2, d_combine_buf,
+                               d_x_slots, dW1, dW2, workspace, stream=None):
+    """moe_expert_backward_checkpoint: expert_backward from the checkpoint that
+    expert_forward_checkpoint left in gu and gu_scale. X is bf16 with
+    X_scale=None, or int8 MXINT8 codes with their scales uint8 [..., d/32]."""
+    w, bf, cap, El = "expert_backward_checkpoint", torch.bfloat16, row_capacity(p), p.e_end - p.e_begin
+    rows = cap if row_src is None else p.T
+    args = (_operand(w, "X", X, bf if X_scale is None else torch.int8, rows * p.d),
+            _operand(w, "X_scale", X_scale, torch.uint8, rows * p.d // 32, optional=True),
+            _operand(w, "row_src", row_src, torch.int32, cap, optional=True),
+            _operand(w, "offsets", offsets, torch.int32, El + 1), _operand(w, "row_dst", row_dst, torch.int32, cap),
+            _operand(w, "gu", gu, torch.int8, cap * 2 * p.f),
+            _operand(w, "gu_scale", gu_scale, torch.uint8, cap * p.f // 16),
+            _operand(w, "W1", W1, bf, El * 2 * p.f * p.d), _operand(w, "W2", W2, bf, El * p.d * p.f),
+            _operand(w, "d_combine_buf", d_combine_buf, bf, cap * p.d),
+            _operand(w, "d_x_slots", d_x_slots, bf, cap * p.d), _operand(w, "dW1", dW1, bf, El * 2 * p.f * p.d),
+            _operand(w, "dW2", dW2, bf, El * p.d * p.f), _operand(w, "workspace", workspace, torch.uint8, 0))
+    _launch(w, stream, (X, X_scale, row_src, offsets, row_dst, gu, gu_scale, W1, W2, d_combine_buf, d_x_slots, dW1, dW2,
+                        workspace),
+            lambda s: lib().moe_expert_backward_checkpoint(ctypes.byref(p), *args, workspace.numel(), s))
 
 
 def check_workspace(p: Problem, workspace, stream=None):

@@ -58,6 +58,7 @@ moe_status_t check_ws(const moe::Layout& L, const void* ws, size_t bytes) {
   return MOE_OK;
 }
 
+bool aligned4(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3) == 0; }
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
 
 // An array of a call. A null one shares bytes with nothing.
@@ -90,11 +91,15 @@ Span workspace_tables(const moe::Layout& L, const void* ws) { return {ws, L.pub.
 // rows up to 4 f bytes).
 bool backward_widths_ok(const moe_problem_t& p) { return p.d <= 1 << 20 && p.f <= 1 << 20; }
 
-// Shapes of the MXFP4 codec: whole blocks, and an element count that 64-bit
-// byte offsets hold with room to spare.
-moe_status_t check_mxfp4_shape(int64_t rows, int64_t cols) {
+// The 8-bit integer sums of K products of codes in [-128, 127] fit 32 bits.
+constexpr int kInt8MaxK = (1 << 17) - 1;
+
+// Shapes of a codec: rows of whole units (blocks of 32, or the 16 codes that
+// keep a row of 8-bit integers 16-byte aligned), and an element count that
+// 64-bit byte offsets hold with room to spare.
+moe_status_t check_codec_shape(int64_t rows, int64_t cols, int unit) {
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARGUMENT;
-  if (cols % 32 || cols > (1ll << 40) || (rows > 0 && cols > (1ll << 46) / rows)) return MOE_ERR_UNSUPPORTED;
+  if (cols % unit || cols > (1ll << 40) || (rows > 0 && cols > (1ll << 46) / rows)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -532,7 +537,7 @@ MOE_API moe_status_t moe_mxfp4_linear2(const moe_problem_t* p, const uint8_t* H,
 
 MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, uint8_t* codes,
                                         uint8_t* scales, void* stream) {
-  moe_status_t st = check_mxfp4_shape(rows, cols);
+  moe_status_t st = check_codec_shape(rows, cols, 32);
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARGUMENT;
@@ -544,7 +549,7 @@ MOE_API moe_status_t moe_mxfp4_quantize(const void* x, int x_fp32, int64_t rows,
 
 MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                                           void* out, int out_fp32, void* stream) {
-  moe_status_t st = check_mxfp4_shape(rows, cols);
+  moe_status_t st = check_codec_shape(rows, cols, 32);
   if (st != MOE_OK) return st;
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out)) return MOE_ERR_INVALID_ARGUMENT;
@@ -553,6 +558,193 @@ MOE_API moe_status_t moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* s
     return MOE_ERR_INVALID_ARGUMENT;
   const hipError_t e = moe::launch_mxfp4_dequantize(codes, scales, rows * cols, out, out_fp32 != 0,
                                                     (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_int8_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, int8_t* codes,
+                                       float* scales, void* stream) {
+  moe_status_t st = check_codec_shape(rows, cols, 16);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned4(scales))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{codes, n}, {scales, (size_t)rows * 4}}, {{x, n * (x_fp32 ? 4 : 2)}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_int8_quantize(x, x_fp32 != 0, rows, cols, codes, scales, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                         void* out, int out_fp32, void* stream) {
+  moe_status_t st = check_codec_shape(rows, cols, 16);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out) || !aligned4(scales))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{out, n * (out_fp32 ? 4 : 2)}}, {{codes, n}, {scales, (size_t)rows * 4}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e =
+      moe::launch_int8_dequantize(codes, scales, rows, cols, out, out_fp32 != 0, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_int8_linear1(const moe_problem_t* p, const int8_t* X, const float* X_scale,
+                                      const int32_t* row_src, const int32_t* offsets, const int8_t* W1,
+                                      const float* W1_scale, void* H, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->d > kInt8MaxK) return MOE_ERR_UNSUPPORTED;
+  if (!X || !X_scale || !offsets || !W1 || !W1_scale || !H) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(X) || !aligned16(X_scale) || !aligned16(W1) || !aligned16(W1_scale) || !aligned16(H))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const size_t rows = row_src ? (size_t)p->T : (size_t)L.cap, w_rows = (size_t)L.E_l * 2 * p->f;
+  const Span out{H, (size_t)L.cap * p->f * 2}, tables = workspace_tables(L, workspace);
+  if (shares_bytes({out, tables}, {{X, rows * p->d},
+                                   {X_scale, rows * 4},
+                                   {row_src, (size_t)L.cap * 4},
+                                   {offsets, ((size_t)L.E_l + 1) * 4},
+                                   {W1, w_rows * p->d},
+                                   {W1_scale, w_rows * 4}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_int8_linear(*p, L, static_cast<char*>(workspace), true, X, X_scale, row_src,
+                                               offsets, nullptr, W1, W1_scale, H, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_int8_linear2(const moe_problem_t* p, const int8_t* H, const float* H_scale,
+                                      const int32_t* offsets, const int32_t* row_dst, const int8_t* W2,
+                                      const float* W2_scale, void* combine_buf, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->f > kInt8MaxK) return MOE_ERR_UNSUPPORTED;
+  if (!H || !H_scale || !offsets || !row_dst || !W2 || !W2_scale || !combine_buf) return MOE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(H) || !aligned16(H_scale) || !aligned16(W2) || !aligned16(W2_scale) || !aligned16(combine_buf))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const size_t w_rows = (size_t)L.E_l * p->d;
+  const Span out{combine_buf, (size_t)L.cap * p->d * (p->flags & MOE_FLAG_BF16_COMBINE_BUF ? 2 : 4)},
+      tables = workspace_tables(L, workspace);
+  if (shares_bytes({out, tables}, {{H, (size_t)L.cap * p->f},
+                                   {H_scale, (size_t)L.cap * 4},
+                                   {offsets, ((size_t)L.E_l + 1) * 4},
+                                   {row_dst, (size_t)L.cap * 4},
+                                   {W2, w_rows * p->f},
+                                   {W2_scale, w_rows * 4}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_int8_linear(*p, L, static_cast<char*>(workspace), false, H, H_scale, nullptr,
+                                               offsets, row_dst, W2, W2_scale, combine_buf, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_mxint8_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, int8_t* codes,
+                                         uint8_t* scales, void* stream) {
+  moe_status_t st = check_codec_shape(rows, cols, 32);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{codes, n}, {scales, n / 32}}, {{x, n * (x_fp32 ? 4 : 2)}})) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_mxint8_quantize(x, x_fp32 != 0, rows * cols, codes, scales, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                           void* out, int out_fp32, void* stream) {
+  moe_status_t st = check_codec_shape(rows, cols, 32);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(out)) return MOE_ERR_INVALID_ARGUMENT;
+  const size_t n = (size_t)(rows * cols);
+  if (shares_bytes({{out, n * (out_fp32 ? 4 : 2)}}, {{codes, n}, {scales, n / 32}})) return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e =
+      moe::launch_mxint8_dequantize(codes, scales, rows * cols, out, out_fp32 != 0, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const void* X, const int32_t* row_src,
+                                                   const int32_t* offsets, const int32_t* row_dst, const void* W1,
+                                                   const void* W2, int8_t* gu, uint8_t* gu_scale, void* combine_buf,
+                                                   void* workspace, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!X || !offsets || !row_dst || !W1 || !W2 || !gu || !gu_scale || !combine_buf) return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {X, W1, W2, (const void*)gu, (const void*)gu_scale, (const void*)combine_buf})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const size_t w = (size_t)L.E_l * p->d * p->f * 2, vals = (size_t)L.cap * 2 * p->f;
+  char* ws = static_cast<char*>(workspace);
+  if (shares_bytes({{gu, vals},
+                    {gu_scale, vals / 32},
+                    {combine_buf, (size_t)L.cap * p->d * (p->flags & MOE_FLAG_BF16_COMBINE_BUF ? 2 : 4)},
+                    workspace_tables(L, workspace),
+                    {ws + L.pub.h, (size_t)L.cap * p->f * 2},
+                    {ws + L.pub.tile_trace, L.pub.tile_trace_capacity * sizeof(moe_tile_record_t)}},
+                   {{X, (row_src ? (size_t)p->T : (size_t)L.cap) * p->d * 2},
+                    {row_src, (size_t)L.cap * 4},
+                    {offsets, ((size_t)L.E_l + 1) * 4},
+                    {row_dst, (size_t)L.cap * 4},
+                    {W1, 2 * w},
+                    {W2, w}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_expert_forward_checkpoint(*p, L, ws, X, row_src, offsets, row_dst, W1, W2, gu,
+                                                             gu_scale, combine_buf, (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(e);
+}
+
+MOE_API size_t moe_checkpoint_workspace_size(const moe_problem_t* p) {
+  if (check_problem(p) != MOE_OK || p->dtype != MOE_DTYPE_BF16 || !backward_widths_ok(*p)) return 0;
+  return moe::checkpoint_layout(*p, moe::make_layout(*p)).total;
+}
+
+MOE_API moe_status_t moe_expert_backward_checkpoint(const moe_problem_t* p, const void* X, const uint8_t* X_scale,
+                                                    const int32_t* row_src, const int32_t* offsets,
+                                                    const int32_t* row_dst, const int8_t* gu, const uint8_t* gu_scale,
+                                                    const void* W1, const void* W2, const void* d_combine_buf,
+                                                    void* d_x_slots, void* dW1, void* dW2, void* workspace,
+                                                    size_t ws_bytes, void* stream) {
+  moe_status_t st = check_problem(p);
+  if (st != MOE_OK) return st;
+  if (p->dtype != MOE_DTYPE_BF16 || !backward_widths_ok(*p)) return MOE_ERR_UNSUPPORTED;
+  if (!X || !offsets || !row_dst || !gu || !gu_scale || !W1 || !W2 || !d_combine_buf || !d_x_slots || !dW1 || !dW2)
+    return MOE_ERR_INVALID_ARGUMENT;
+  for (const void* q : {X, (const void*)X_scale, (const void*)gu, (const void*)gu_scale, W1, W2, d_combine_buf,
+                        (const void*)d_x_slots, (const void*)dW1, (const void*)dW2})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe::Layout L = moe::make_layout(*p);
+  if ((st = check_ws(L, workspace, ws_bytes)) != MOE_OK) return st;
+  const moe::BackwardLayout B = moe::checkpoint_layout(*p, L);
+  if (ws_bytes < B.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t slots = (size_t)L.cap * p->d * 2, w = (size_t)L.E_l * p->d * p->f * 2, vals = (size_t)L.cap * 2 * p->f,
+               x = (row_src ? (size_t)p->T : (size_t)L.cap) * p->d;
+  // the outputs, and the tables and intermediates this call writes in the workspace
+  if (shares_bytes({{d_x_slots, slots},
+                    {dW1, 2 * w},
+                    {dW2, w},
+                    workspace_tables(L, workspace),
+                    {static_cast<char*>(workspace) + B.gu, B.total - B.gu}},
+                   {{X, X_scale ? x : 2 * x},
+                    {X_scale, x / 32},
+                    {row_src, (size_t)L.cap * 4},
+                    {offsets, ((size_t)L.E_l + 1) * 4},
+                    {row_dst, (size_t)L.cap * 4},
+                    {gu, vals},
+                    {gu_scale, vals / 32},
+                    {W1, 2 * w},
+                    {W2, w},
+                    {d_combine_buf, slots}}))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const hipError_t e = moe::launch_expert_backward_checkpoint(
+      *p, L, static_cast<char*>(workspace), X, X_scale, row_src, offsets, row_dst, gu, gu_scale, W1, W2, d_combine_buf,
+      d_x_slots, dW1, dW2, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(e);
 }
 

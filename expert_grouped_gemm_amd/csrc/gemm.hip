@@ -326,6 +326,52 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
   return launch_gemm_w4a4(P, G, s);
 }
 
+// One Linear of the experts on 8-bit integers (see moe_int8_linear1 /
+// moe_int8_linear2), as a launch of the persistent GEMM.
+hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const int8_t* A,
+                              const float* A_scale, const int32_t* row_src, const int32_t* offsets,
+                              const int32_t* row_dst, const int8_t* W, const float* W_scale, void* out,
+                              hipStream_t s) {
+  const int G = gemm_grid(p);
+  if (G <= 0) return hipErrorInvalidDevice;
+  const hipError_t e =
+      first ? launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP, ARG_ERR_LINEAR1, s)
+            : launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP | ARG_ERR_LINEAR1, 0, s);
+  if (e != hipSuccess) return e;
+  GemmParams P = gemm_params(p, L, ws, G, A, nullptr, row_dst, W, nullptr, W, nullptr, out, nullptr, 0);
+  P.Ar = A_scale;
+  P.Wc = W_scale;
+  P.H = reinterpret_cast<uint8_t*>(first ? out : const_cast<int8_t*>(A));
+  P.a_src = row_src;
+  P.a_k = p.k;
+  P.trace = nullptr;
+  P.mode = first ? MODE_SEP_L1 : MODE_SEP_L2;
+  return launch_gemm_int8(P, G, s);
+}
+
+// The experts' products in bf16 with a checkpoint of Linear-1's outputs (see
+// moe_expert_forward_checkpoint): Linear-1 is the kernel whose epilogue also
+// leaves gate and up in MXINT8, Linear-2 the bf16 kernel's own.
+hipError_t launch_expert_forward_checkpoint(const moe_problem_t& p, const Layout& L, char* ws, const void* X,
+                                            const int32_t* row_src, const int32_t* offsets, const int32_t* row_dst,
+                                            const void* W1, const void* W2, int8_t* gu, uint8_t* gu_scale,
+                                            void* combine_buf, hipStream_t s) {
+  const int G = gemm_grid(p);
+  if (G <= 0) return hipErrorInvalidDevice;
+  hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP, ARG_ERR_LINEAR1, s);
+  if (e != hipSuccess) return e;
+  GemmParams P = gemm_params(p, L, ws, G, X, nullptr, row_dst, W1, nullptr, W2, nullptr, combine_buf, nullptr, 0);
+  P.a_src = row_src;
+  P.a_k = p.k;
+  P.gu = gu;
+  P.gue = gu_scale;
+  P.mode = MODE_SEP_L1;
+  e = launch_gemm_checkpoint(P, G, s);
+  if (e != hipSuccess) return e;
+  P.mode = MODE_SEP_L2;
+  return launch_gemm_bf16(P, G, s);
+}
+
 // moe_layer_forward's expert GEMMs: the fused dispatch kernel has already
 // planned the row bands, and Linear-1 gathers each band's rows from X
 // through row_src (assignment a is token a / k).

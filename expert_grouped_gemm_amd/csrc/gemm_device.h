@@ -109,6 +109,13 @@ struct GemmParams {
   // a_src[r] / a_k (X is then the token rows, not X_perm); null: X_perm rows
   const int32_t* a_src;
   int a_k;
+  // 8-bit integers: the scale of each row of A (of each token where gathered)
+  // and of each weight row (Linear-1 [E_l, 2f], Linear-2 [E_l, d])
+  const float* Ar;
+  const float* Wc;
+  // checkpoint: gate and up of every row in MXINT8, [cap, 2f] and [cap, 2f/32]
+  int8_t* gu;
+  uint8_t* gue;
 };
 
 // Launch the persistent expert-GEMM kernel of one operand type (bf16 in
@@ -119,6 +126,8 @@ hipError_t launch_gemm_bf16(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_fp8(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_w4a8(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_w4a4(const GemmParams& P, int G, hipStream_t s);
+hipError_t launch_gemm_int8(const GemmParams& P, int G, hipStream_t s);
+hipError_t launch_gemm_checkpoint(const GemmParams& P, int G, hipStream_t s);  // Linear-1
 const void* gemm_kernel_bf16();
 
 namespace {
@@ -129,6 +138,7 @@ typedef __attribute__((address_space(3))) uint8_t lds_t;
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
@@ -148,10 +158,11 @@ struct Tile {
   int ktiles;             // K bytes / stage_k_bytes
   int krot;               // pipeline stage kt streams K slice (kt + krot) mod ktiles
   bool once;              // the expert's only row band: each weight byte is read once per launch
-  // fp8 activations only
-  const float* As;        // row scales of K block 0 for the band's first row (next block: + cap)
-  const float* Sg;        // fp8 weights: block scales of the first half along K (one per 128-byte stage)
-  const float* Su;        // fp8 weights: block scales of the second half
+  // fp8 activations and 8-bit integers only
+  const float* As;        // row scales of K block 0 for the band's first row (next block: + cap); integers: of row 0 of A
+  const float* Sg;        // fp8 weights: block scales of the first half along K (one per 128-byte stage);
+                          // integers: scales of the tile's weight rows, first half
+  const float* Su;        // ... of the second half
   int cap_stride;         // elements between consecutive K blocks of the row scales
   // MXFP4 weights only: E8M0 bytes, K/32 per weight row (4 per 128-wide stage)
   const uint8_t* Eg;      // scale row of the first weight row of the first half
@@ -176,12 +187,17 @@ struct Tile {
 // Operand types of the expert GEMM (the template parameter OT): bf16
 // activations and weights; e4m3 activations and e4m3 weights with fp32
 // 128x128 block scales; e4m3 activations and MXFP4 weights (E2M1 elements,
-// one E8M0 scale per 32 along K); MXFP4 activations and MXFP4 weights.
-enum OperandType { OT_BF16 = 0, OT_FP8 = 1, OT_W4A8 = 2, OT_W4A4 = 3 };
+// one E8M0 scale per 32 along K); MXFP4 activations and MXFP4 weights; 8-bit
+// integers with one fp32 scale per row of either; bf16 whose Linear-1 also
+// leaves its SwiGLU inputs in MXINT8.
+enum OperandType { OT_BF16 = 0, OT_FP8 = 1, OT_W4A8 = 2, OT_W4A4 = 3, OT_I8 = 4, OT_CKPT = 5 };
+__host__ __device__ constexpr bool bf16_operands(int OT) { return OT == OT_BF16 || OT == OT_CKPT; }
+// Operand types without scales inside the K loop: their stages are the rows alone.
+__host__ __device__ constexpr bool plain_stages(int OT) { return bf16_operands(OT) || OT == OT_I8; }
 __host__ __device__ constexpr bool mxfp4_weights(int OT) { return OT == OT_W4A8; }  // against e4m3 activations
 __host__ __device__ constexpr bool e4m3_acts(int OT) { return OT == OT_FP8 || OT == OT_W4A8; }
 // Operand types whose tiles may issue their successor's first stages (see Chain).
-__host__ __device__ constexpr bool chains_tiles(int OT) { return OT == OT_BF16 || OT == OT_W4A4; }
+__host__ __device__ constexpr bool chains_tiles(int OT) { return plain_stages(OT) || OT == OT_W4A4; }
 
 // K bytes per row per pipeline stage: 64 bf16 values, or for fp8 one 128-wide
 // scale block of e4m3 values, or 256 MXFP4 values (both operands). (64-byte bf16 stages, which double the ring
@@ -261,7 +277,7 @@ __host__ __device__ constexpr int stage_b_rows_per_round(int OT) {
 }
 __host__ __device__ constexpr int stage_loads(int MB, int NNB, int OT) {
   return (MB * 32 + stage_a_rows_per_round(OT) - 1) / stage_a_rows_per_round(OT) +
-         NNB * 64 / stage_b_rows_per_round(OT) + (OT == OT_W4A4 ? (MB + 3) / 4 + NNB / 2 : OT ? 2 : 0);
+         NNB * 64 / stage_b_rows_per_round(OT) + (OT == OT_W4A4 ? (MB + 3) / 4 + NNB / 2 : e4m3_acts(OT) ? 2 : 0);
 }
 
 // Wavefront grid of a tile of width NNB: WM wavefront rows x WN wavefront
@@ -376,7 +392,7 @@ __device__ __forceinline__ void issue_load(const Tile& t, int kt, lds_t* st, int
       const uint8_t* g = base + (uint32_t)((r & (half - 1)) * (uint32_t)t.epitch + kt * 8 + dw * 4);
       __builtin_amdgcn_global_load_lds(g, ss + kBM * 8 + r0 * 8, 4, 0, 0);
     }
-  } else if constexpr (OT != OT_BF16) {
+  } else if constexpr (e4m3_acts(OT)) {
     lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     if (j == NA + NBW) {
       // the 256 row scales: kBM / NW per wavefront, one 4-byte lane each
@@ -497,7 +513,18 @@ constexpr int load_points() { return NMB >= 3 ? 1 : 4; }
 struct NoLoads {
   __device__ void operator()(int) const {}
 };
-template <int NMB, int NNB, int NL = 0, class Issue = NoLoads>
+// The product of one 16-byte chunk per lane of either operand: 16 bf16 values of
+// K, or 32 integers, whose exact 32-bit sums the accumulator registers hold as
+// they are (scale_int8 turns them into fp32 after the K loop).
+template <int OT>
+__device__ __forceinline__ f32x16 mfma_chunk(bf16x8 b, bf16x8 a, f32x16 acc) {
+  if constexpr (OT == OT_I8)
+    return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, b),
+                                                                            __builtin_bit_cast(i32x4, a),
+                                                                            __builtin_bit_cast(i32x16, acc), 0, 0, 0));
+  else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, acc, 0, 0, 0);
+}
+template <int NMB, int NNB, int OT, int NL = 0, class Issue = NoLoads>
 __device__ __forceinline__ void compute_stage(const lds_t* sa, const lds_t* sb, int tid,
                                               f32x16 (&acc)[NMB][WaveGrid<NNB, false>::NCB],
                                               const Issue& issue = Issue()) {
@@ -533,7 +560,7 @@ __device__ __forceinline__ void compute_stage(const lds_t* sa, const lds_t* sb, 
     for (int mi = 0; mi < NMB; ++mi)
 #pragma unroll
       for (int nb = 0; nb < G::NCB; ++nb)
-        acc[mi][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[ks & 1][nb], fa[ks & 1][mi], acc[mi][nb], 0, 0, 0);
+        acc[mi][nb] = mfma_chunk<OT>(fb[ks & 1][nb], fa[ks & 1][mi], acc[mi][nb]);
   }
 }
 
@@ -713,13 +740,13 @@ __device__ __forceinline__ void compute_any(const Tile& t, const lds_t* st, int 
   } else if constexpr (mxfp4_weights(OT)) {
     const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     compute_stage_w4<NMB, NNB>(st, st + stage_a_bytes(MB, OT), ss, tid, acc);
-  } else if constexpr (OT) {
+  } else if constexpr (e4m3_acts(OT)) {
     static_assert(stage_k_bytes(true) == 128, "an fp8 stage is one 128-wide scale block");
     const lds_t* ss = st + stage_a_bytes(MB, OT) + stage_b_bytes(NNB, OT);
     const float swg = *(const lds_f32*)(ss + kBM * 4), swu = *(const lds_f32*)(ss + kBM * 4 + 4);
     compute_stage_fp8<NMB, NNB>(st, st + stage_a_bytes(MB, OT), ss, swg, swu, tid, acc);
   } else {
-    compute_stage<NMB, NNB>(st, st + stage_a_bytes(MB, OT), tid, acc);
+    compute_stage<NMB, NNB, OT>(st, st + stage_a_bytes(MB, OT), tid, acc);
   }
 }
 
@@ -745,6 +772,63 @@ constexpr bool stages_block_in_lds() { return e4m3_acts(OT) && L1 && NNB * 32 ==
 // value is below 1e-36 in magnitude.
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f)) * u;
+}
+
+// 8-bit integers: the accumulators' 32-bit sums as fp32 (rounded above 2^24),
+// times the row's scale, times the weight row's.
+template <int NMB, int NNB>
+__device__ __forceinline__ void scale_int8(const Tile& t, int tid, f32x16 (&acc)[NMB][WaveGrid<NNB, OT_I8>::NCB]) {
+  using G = WaveGrid<NNB, OT_I8>;
+  const int lane = tid & 63, w = tid >> 6, wm = w % G::WM, wn = w / G::WM;
+  const int lr = lane & 31, hi = lane >> 5;
+  float sx[NMB];
+#pragma unroll
+  for (int mi = 0; mi < NMB; ++mi) {
+    const int m = (wm + G::WM * mi) * 32 + lr;
+    sx[mi] = 0.0f;
+    if (m < t.rows) sx[mi] = t.As[t.a_src ? t.a_src[t.row0 + m] / t.a_k : t.row0 + m];
+  }
+#pragma unroll
+  for (int nb = 0; nb < G::NCB; ++nb) {
+    const float* half = nb < G::CPH ? t.Sg : t.Su;
+    float4 sw[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sw[q] = *reinterpret_cast<const float4*>(half + wave_col<NNB, OT_I8>(0, nb % G::CPH, wn, 0) + 8 * q + 4 * hi);
+#pragma unroll
+    for (int mi = 0; mi < NMB; ++mi)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float s[4] = {sw[q].x, sw[q].y, sw[q].z, sw[q].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[mi][nb][4 * q + e] = (float)__float_as_int(acc[mi][nb][4 * q + e]) * sx[mi] * s[e];
+      }
+  }
+}
+
+// Checkpoint: a row's 32 values of accumulator block a (gate or up columns col
+// .. col + 31) in MXINT8. The row is held by lanes l and l + 32, 16 values each
+// in runs of four columns; after two swaps of the halves lane l holds the
+// codes of the first 16 columns and lane l + 32 those of the other 16.
+__device__ __forceinline__ void store_mxint8(const GemmParams& P, const f32x16& a, size_t row, int col, int hi) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+  const uint32_t byte = mxint8_scale(m);
+  const float inv = mxint8_inverse_step(byte);
+  uint32_t c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    c[q] = low_bytes(mxint8_code(a[4 * q], inv), mxint8_code(a[4 * q + 1], inv), mxint8_code(a[4 * q + 2], inv),
+                     mxint8_code(a[4 * q + 3], inv));
+    if (byte == 255) c[q] = 0;
+  }
+  const auto s02 = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+  const auto s13 = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+  *reinterpret_cast<uint4*>(P.gu + row * (2 * (size_t)P.f) + col + 16 * hi) = make_uint4(s02[0], s02[1], s13[0], s13[1]);
+  if (hi == 0) P.gue[row * (size_t)(P.f >> 4) + (col >> 5)] = (uint8_t)byte;
 }
 
 template <int NMB, int NNB, bool L1, int OT>
@@ -808,6 +892,11 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& P, const Tile& t
           }
           const int col = wave_col<NNB, OT>(0, c, wn, 0) + 8 * q + 4 * hi;
           *reinterpret_cast<uint2*>(hrow + col) = make_uint2(packed[0], packed[1]);
+        }
+        if constexpr (OT == OT_CKPT) {
+          const int col = t.n * (NNB * 32) + wave_col<NNB, OT>(0, c, wn, 0);
+          store_mxint8(P, acc[mi][c], (size_t)t.row0 + m, col, hi);
+          store_mxint8(P, acc[mi][G::CPH + c], (size_t)t.row0 + m, P.f + col, hi);
         }
       }
     } else {
@@ -1016,8 +1105,8 @@ __device__ __forceinline__ void tile_body(const GemmParams& P, const Tile& t0, l
       if constexpr (loader) {
         const int ks = kslice<OT>(t, kt + S - 1);
         lds_t* st = lds + wr * SB;
-        if constexpr (NMB > 0 && OT == OT_BF16) {
-          compute_stage<NMB, NNB, LD>(lds + rd * SB, lds + rd * SB + stage_a_bytes(MB, OT), tid, acc,
+        if constexpr (NMB > 0 && plain_stages(OT)) {
+          compute_stage<NMB, NNB, OT, LD>(lds + rd * SB, lds + rd * SB + stage_a_bytes(MB, OT), tid, acc,
                                       [&](int j) { issue_load<MB, NNB, OT, NT>(t, ks, st, tid, j); });
         } else {
           // e4m3 activations: the whole stage at once, then the MFMAs
@@ -1057,6 +1146,7 @@ __device__ __forceinline__ void tile_body(const GemmParams& P, const Tile& t0, l
   // (also one without row blocks) then meets at a barrier before the next
   // tile's loads refill the ring.
   const bool stage = !L1 && !ch.issued && !P.c_bf16;
+  if constexpr (NMB > 0 && OT == OT_I8) scale_int8<NMB, NNB>(t, tid, acc);
   if constexpr (NMB > 0) epilogue<NMB, NNB, L1, OT>(P, t, tid, acc, lds, stage);
   if (stage) lds_barrier();
 }
@@ -1303,7 +1393,7 @@ __device__ __forceinline__ void set_khalf(Tile& t, int K) {
 
 template <bool L1, int OT>
 __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int nnb) {
-  constexpr int esz = OT ? 1 : 2;
+  constexpr int esz = bf16_operands(OT) ? 2 : 1;
   Tile t;
   const int eb = P.band_expert[p], e = eb & kBandExpertMask;
   t.once = (eb & kBandSingle) != 0;
@@ -1336,7 +1426,11 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
       const uint8_t* Es = P.W1e + (size_t)e * 2 * P.f * t.epitch;
       t.Eg = Es + (size_t)(n * bn) * t.epitch;
       t.Eu = Es + (size_t)(P.f + n * bn) * t.epitch;
-    } else if constexpr (OT) {
+    } else if constexpr (OT == OT_I8) {
+      t.As = P.Ar;
+      t.Sg = P.Wc + (size_t)e * 2 * P.f + n * bn;
+      t.Su = t.Sg + P.f;
+    } else if constexpr (e4m3_acts(OT)) {
       const int db = P.d >> 7, fb2 = (2 * P.f) >> 7;
       t.As = P.Xs + t.row0;
       t.Sg = P.W1s + ((size_t)e * fb2 + (n * bn) / 128) * db;
@@ -1361,7 +1455,11 @@ __device__ __forceinline__ Tile make_tile(const GemmParams& P, int p, int n, int
       t.epitch = (size_t)P.f / 32;
       t.Eg = P.W2e + ((size_t)e * P.d + (size_t)n * bn) * t.epitch;
       t.Eu = t.Eg + (size_t)(bn / 2) * t.epitch;
-    } else if constexpr (OT) {
+    } else if constexpr (OT == OT_I8) {
+      t.As = P.Ar;
+      t.Sg = P.Wc + (size_t)e * P.d + n * bn;
+      t.Su = t.Sg + bn / 2;
+    } else if constexpr (e4m3_acts(OT)) {
       t.As = P.Hs + t.row0;
       t.Sg = P.W2s + ((size_t)e * (P.d >> 7) + (n * bn) / 128) * (P.f >> 7);
       t.Su = P.W2s + ((size_t)e * (P.d >> 7) + (n * bn + bn / 2) / 128) * (P.f >> 7);
@@ -1464,7 +1562,11 @@ __global__ __launch_bounds__(gemm_threads(OT), 1) void moe_gemm_kernel(GemmParam
   const int Pb = P.meta[META_P];
   int p, n;
   Chain none;  // the fused schedules prefetch nothing across tiles
-  if constexpr (OT == OT_W4A4) {  // the two Linears are calls of their own
+  if constexpr (OT == OT_CKPT) {  // Linear-2 is the bf16 kernel's
+    separate_tiles<true, OT>(P, Pb, P.N1, P.nnb1, lid, G, lds);
+    return;
+  }
+  if constexpr (OT == OT_W4A4 || OT == OT_I8) {  // the two Linears are calls of their own
     if (P.mode == MODE_SEP_L1) separate_tiles<true, OT>(P, Pb, P.N1, P.nnb1, lid, G, lds);
     else separate_tiles<false, OT>(P, Pb, P.N2, P.nnb2, lid, G, lds);
     return;

@@ -38,10 +38,11 @@ constexpr int kMetaTag = 0x4D6F4531;
 // whole word (the workspace may hold anything before its first use); inside
 // moe_layer_forward the expert GEMM clears only its own bits, so the
 // dispatch's report survives until moe_check_workspace reads it. The calls that
-// follow others on the same arrays (the MXFP4 Linears, the experts' gradient)
-// clear the bits of their own checks, ARG_ERR_PLAN, and leave what the calls
-// before them reported: the dispatch, a forward's timed-out wait, and
-// ARG_ERR_LINEAR1, that Linear-1 was rejected and left H as it was.
+// follow others on the same arrays (the MXFP4 and int8 Linears, the experts'
+// gradients, the forward pass with a checkpoint) clear the bits of their own
+// checks, ARG_ERR_PLAN, and leave what the calls before them reported: the
+// dispatch, a forward's timed-out wait, and ARG_ERR_LINEAR1, that Linear-1 (or
+// the checkpoint's forward pass) was rejected and left its outputs as they were.
 enum ArgErr {
   ARG_ERR_DISPATCH_CAP = 1, ARG_ERR_OFFSETS = 2, ARG_ERR_ROW_DST = 4, ARG_ERR_ROW_SRC = 8, ARG_ERR_LINEAR1 = 16,
   ARG_ERR_PLAN = 14, ARG_ERR_ALL = 31
@@ -207,6 +208,15 @@ hipError_t launch_expert_backward(const moe_problem_t& p, const Layout& L, char*
                                   const void* W1, const void* W2, const void* dO, void* dxs, void* dW1, void* dW2,
                                   hipStream_t s);
 
+// moe_expert_backward_checkpoint's intermediates: no gate and up values, and
+// the token rows always (their codes are expanded in expert order).
+BackwardLayout checkpoint_layout(const moe_problem_t& p, const Layout& L);
+hipError_t launch_expert_backward_checkpoint(const moe_problem_t& p, const Layout& L, char* ws, const void* X,
+                                             const uint8_t* X_scale, const int32_t* row_src, const int32_t* offsets,
+                                             const int32_t* row_dst, const int8_t* gu, const uint8_t* gu_scale,
+                                             const void* W1, const void* W2, const void* dO, void* dxs, void* dW1,
+                                             void* dW2, hipStream_t s);
+
 // One Linear on MXFP4 operands (validated arguments).
 hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const uint8_t* A,
                                const uint8_t* A_scale, const int32_t* row_src, const int32_t* offsets,
@@ -225,6 +235,28 @@ hipError_t launch_dispatch_backward(const moe_problem_t& p, const void* d_x_slot
 hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t n, uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t n, void* out, bool f32,
                                    hipStream_t s);
+
+// Rows of 8-bit integers with a scale each, and MXINT8 over n elements (n % 32
+// == 0; validated arguments).
+hipError_t launch_int8_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                                hipStream_t s);
+hipError_t launch_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols, void* out,
+                                  bool f32, hipStream_t s);
+hipError_t launch_mxint8_quantize(const void* x, bool f32, int64_t n, int8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mxint8_dequantize(const int8_t* codes, const uint8_t* scales, int64_t n, void* out, bool f32,
+                                    hipStream_t s);
+
+// One Linear on 8-bit integers (validated arguments).
+hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const int8_t* A,
+                              const float* A_scale, const int32_t* row_src, const int32_t* offsets,
+                              const int32_t* row_dst, const int8_t* W, const float* W_scale, void* out,
+                              hipStream_t s);
+
+// moe_expert_forward_checkpoint (validated arguments).
+hipError_t launch_expert_forward_checkpoint(const moe_problem_t& p, const Layout& L, char* ws, const void* X,
+                                            const int32_t* row_src, const int32_t* offsets, const int32_t* row_dst,
+                                            const void* W1, const void* W2, int8_t* gu, uint8_t* gu_scale,
+                                            void* combine_buf, hipStream_t s);
 
 // Owner-aligned return path (validated arguments; see moe_owner_plan,
 // moe_owner_gather and moe_segment_copy).
@@ -279,6 +311,41 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
+// MXINT8 (one E8M0 scale per 32 elements, element = code * scale / 64). The
+// scale byte of a block whose largest magnitude has the fp32 bits m: the
+// exponent of m, at least 7 (an element's step, 2^(byte - 133), is then a
+// normal number); 127 for zeros; 255 (NaN) if an element is infinite or NaN.
+__device__ __forceinline__ uint32_t mxint8_scale(uint32_t m) {
+  return m >= 0x7F800000u ? 255u : m == 0 ? 127u : max(m >> 23, 7u);
+}
+// 1 / step, 2^(133 - byte); byte 7 .. 254 (255 gives some finite number).
+__device__ __forceinline__ float mxint8_inverse_step(uint32_t byte) { return __uint_as_float((260u - byte) << 23); }
+// The step, 2^(byte - 133); NaN for byte 255.
+__device__ __forceinline__ float mxint8_step(uint32_t byte) {
+  return byte == 255 ? __builtin_nanf("") : ldexpf(1.0f, (int)byte - 133);
+}
+// A code in the low byte of the result: x / step is exact, is bounded, and
+// rounds to nearest even in the addition of 1.5 2^23.
+__device__ __forceinline__ uint32_t mxint8_code(float x, float inverse_step) {
+  return __float_as_uint(__builtin_amdgcn_fmed3f(x * inverse_step, -127.0f, 127.0f) + 12582912.0f);
+}
+// Eight codes as values (each exact, in bf16 too).
+__device__ __forceinline__ void mxint8_values8(uint2 c, float step, float (&v)[8]) {
+  const int w[2] = {(int)c.x, (int)c.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = (float)(int8_t)w[i] * step;
+    v[4 * i + 1] = (float)(int8_t)(w[i] >> 8) * step;
+    v[4 * i + 2] = (float)(int8_t)(w[i] >> 16) * step;
+    v[4 * i + 3] = (float)(w[i] >> 24) * step;
+  }
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(b, a, 0x0C0C0400u) | __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
 }
 
 // Eight consecutive columns (8 c .. 8 c + 7) of combine-buffer row p as fp32.

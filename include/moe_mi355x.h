@@ -195,8 +195,9 @@ typedef struct moe_workspace_layout {
                                             errors (bits: 1 = more local assignments than the row
                                             capacity, 2 = offsets not monotone or past the row
                                             capacity, 4 = a row_dst outside the row capacity,
-                                            8 = a row_src outside [0, T*k), 16 = moe_mxfp4_linear1
-                                            rejected its offsets or row_src) */
+                                            8 = a row_src outside [0, T*k), 16 = moe_mxfp4_linear1,
+                                            moe_int8_linear1 or moe_expert_forward_checkpoint
+                                            rejected its offsets or row indices) */
   size_t tile_trace;    /* moe_tile_record_t [tile_trace_capacity]; empty without MOE_FLAG_TILE_TRACE */
   size_t tile_trace_capacity;  /* records (a bound on the tiles of one call) */
   size_t total;         /* = moe_workspace_size */
@@ -307,11 +308,12 @@ MOE_API moe_status_t moe_layer_forward(const moe_problem_t* p, const void* X, co
  * MOE_ERR_DEADLOCK if a persistent-pipeline wait of the most recent
  * expert-GEMM call on this workspace timed out, MOE_ERR_INVALID_ARGUMENT if a
  * device-side check of the last dispatch or expert-GEMM call failed (its
- * outputs are then invalid). moe_mxfp4_linear1, moe_mxfp4_linear2 and
- * moe_expert_backward follow other calls of a layer and leave their reports
- * (of the dispatch, of a forward that timed out, and in Linear-2 that of
- * Linear-1): one check after the last call covers them all. Clears both
- * words. */
+ * outputs are then invalid). moe_mxfp4_linear1, moe_mxfp4_linear2, their int8
+ * forms, moe_expert_backward and the checkpoint calls follow other calls of a
+ * layer and leave their reports (of the dispatch, of a forward that timed out,
+ * in Linear-2 that of Linear-1, and in the backward pass those and that of the
+ * forward pass with a checkpoint): one check after the last call covers them
+ * all. Clears both words. */
 MOE_API moe_status_t moe_check_workspace(const moe_problem_t* p, void* workspace, size_t ws_bytes,
                                          void* stream);
 
@@ -423,7 +425,7 @@ MOE_API moe_status_t moe_segment_copy_wait(const moe_problem_t* p, const float* 
 /* Gradients of the layer's two permutations, for a training step. Both work
  * on any operand type of p (they touch none of the experts' operands).
  *
- * For these two, moe_expert_backward and the MXFP4 calls below, an output that
+ * For these two, moe_expert_backward and the calls below it, an output that
  * shares bytes with an input or with another output (or, where there is a
  * workspace, with the parts of it that the call writes) is
  * MOE_ERR_INVALID_ARGUMENT.
@@ -542,6 +544,111 @@ MOE_API moe_status_t moe_mxfp4_linear2(const moe_problem_t* p, const uint8_t* H,
                                        const int32_t* offsets, const int32_t* row_dst, const uint8_t* W2,
                                        const uint8_t* W2_scale, void* combine_buf, void* workspace, size_t ws_bytes,
                                        void* stream);
+
+/* 8-bit integers with one fp32 scale per row (a token, or a weight row: an
+ * output channel). x [rows, cols], cols % 16 == 0, rows >= 0, DEVICE memory;
+ * codes int8 [rows, cols], scales fp32 [rows]. x, out and codes 16-byte aligned.
+ *
+ * moe_int8_quantize (x fp32 if x_fp32, else bf16): scale = amax / 127 (in fp32;
+ * at least 2^-126, at most the largest whose 127-fold is finite, and 1 for a row
+ * of zeros), code = 127 x / amax (x / scale at
+ * that least scale) rounded to nearest even, exactly: -127 .. 127. A row with an
+ * infinite or NaN element gets the scale NaN and codes 0: every value read back
+ * from it, and every product with it, is NaN.
+ *
+ * moe_int8_dequantize (out fp32 if out_fp32, else bf16): code * scale in fp32,
+ * rounded once more for bf16. Any code and scale are taken. */
+MOE_API moe_status_t moe_int8_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, int8_t* codes,
+                                       float* scales, void* stream);
+MOE_API moe_status_t moe_int8_dequantize(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
+                                         void* out, int out_fp32, void* stream);
+
+/* The experts' Linears on 8-bit integers (W8A8 with a scale for each token and
+ * each output channel), tokens and weights as moe_int8_quantize leaves them. Of
+ * p the shape, the row capacity, the flags and the grid are used, as in the
+ * MXFP4 Linears. A layer forward is
+ *   moe_int8_quantize(X) -> moe_int8_linear1 -> moe_int8_quantize(H)
+ *   -> moe_int8_linear2 -> moe_combine.
+ *
+ * moe_int8_linear1: X int8 [T, d], X_scale fp32 [T] with row_src int32 [cap]
+ * (row r reads token row_src[r] / k), or, with row_src NULL, X int8 [cap, d]
+ * and X_scale [cap] already in expert order; W1 int8 [E_l, 2f, d], W1_scale
+ * fp32 [E_l, 2f]. H bf16 [cap, f] out: row r = silu(g) * u, rounded once, of the
+ * products (g, u) = (W1[e] x) * X_scale * W1_scale.
+ *
+ * moe_int8_linear2: H int8 [cap, f], H_scale fp32 [cap] in expert order; W2
+ * int8 [E_l, d, f], W2_scale fp32 [E_l, d]. combine_buf [cap, d] out (fp32, or
+ * bf16 with MOE_FLAG_BF16_COMBINE_BUF): row row_dst[r] = (W2[e] h) * H_scale *
+ * W2_scale.
+ *
+ * The sums over K are exact (32-bit integers), which takes d (Linear-1) and f
+ * (Linear-2) below 2^17 (MOE_ERR_UNSUPPORTED otherwise); a sum is then rounded to
+ * fp32 and multiplied in fp32 by the row's scale, then the channel's. Rows past
+ * the last stay as they were. Every array 16-byte aligned. Device-side checks
+ * as in moe_mxfp4_linear1 and moe_mxfp4_linear2; if one fails nothing is
+ * computed and the output is left as it was. */
+MOE_API moe_status_t moe_int8_linear1(const moe_problem_t* p, const int8_t* X, const float* X_scale,
+                                      const int32_t* row_src, const int32_t* offsets, const int8_t* W1,
+                                      const float* W1_scale, void* H, void* workspace, size_t ws_bytes,
+                                      void* stream);
+MOE_API moe_status_t moe_int8_linear2(const moe_problem_t* p, const int8_t* H, const float* H_scale,
+                                      const int32_t* offsets, const int32_t* row_dst, const int8_t* W2,
+                                      const float* W2_scale, void* combine_buf, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
+/* MXINT8 codec (OCP MXINT8: 8-bit integers, one E8M0 scale byte per 32
+ * consecutive elements of a row; the value is code * scale / 64). x [rows,
+ * cols], cols % 32 == 0, rows >= 0, DEVICE memory; codes int8 [rows, cols],
+ * scales uint8 [rows, cols/32]. x, out and codes 16-byte aligned. The 8-bit
+ * form in which a training step keeps its activations (see
+ * moe_expert_forward_checkpoint).
+ *
+ * moe_mxint8_quantize (x fp32 if x_fp32, else bf16): per block, scale =
+ * 2^floor(log2 amax), at least 2^-120 (byte 7; byte 127 for a block of zeros),
+ * codes = 64 x / scale rounded to nearest even, saturating at +-127. A block with
+ * an infinite or NaN element gets the scale byte 255 (NaN) and codes 0.
+ *
+ * moe_mxint8_dequantize (out fp32 if out_fp32, else bf16): the values, exact in
+ * either type (the code -128 at scale byte 254, which the quantiser does not
+ * write, is infinity). */
+MOE_API moe_status_t moe_mxint8_quantize(const void* x, int x_fp32, int64_t rows, int64_t cols, int8_t* codes,
+                                         uint8_t* scales, void* stream);
+MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                           void* out, int out_fp32, void* stream);
+
+/* The experts' products of a training step with 8-bit activation checkpoints:
+ * the forward pass leaves the SwiGLU inputs in MXINT8, 2f (1 + 1/32) bytes a
+ * row, and the backward pass takes them from there instead of multiplying the
+ * tokens with W1 again (a quarter of moe_expert_backward's operations). bf16
+ * only (MOE_ERR_UNSUPPORTED otherwise).
+ *
+ * moe_expert_forward_checkpoint: moe_expert_forward (bf16; its combine_buf, bit
+ * for bit, in the separate schedule) on the tokens X bf16 [T, d] through row_src
+ * int32 [cap], or with row_src NULL on rows in expert order [cap, d].
+ *   gu int8 [cap, 2f], gu_scale uint8 [cap, 2f/32] out: the fp32 products
+ *   W1[e] x of row r, gate [0, f) and up [f, 2f), as moe_mxint8_quantize leaves
+ *   them. Rows past the last stay as they were.
+ * workspace: moe_workspace_size(p). Device-side checks as in
+ * moe_mxfp4_linear1 (offsets, row_src, row_dst): if one fails no output is
+ * written.
+ *
+ * moe_expert_backward_checkpoint: moe_expert_backward with the gate and up
+ * values read from gu and gu_scale. X is bf16 as there (X_scale NULL), or int8
+ * MXINT8 codes of the same shape with X_scale uint8 [rows, d/32]. Its roundings
+ * and checks are moe_expert_backward's, d and f at most 2^20; every array
+ * 16-byte aligned. workspace: moe_checkpoint_workspace_size(p) bytes (0 for an
+ * invalid or non-bf16 problem), which serves the forward calls too. */
+MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const void* X, const int32_t* row_src,
+                                                   const int32_t* offsets, const int32_t* row_dst, const void* W1,
+                                                   const void* W2, int8_t* gu, uint8_t* gu_scale, void* combine_buf,
+                                                   void* workspace, size_t ws_bytes, void* stream);
+MOE_API size_t moe_checkpoint_workspace_size(const moe_problem_t* p);
+MOE_API moe_status_t moe_expert_backward_checkpoint(const moe_problem_t* p, const void* X, const uint8_t* X_scale,
+                                                    const int32_t* row_src, const int32_t* offsets,
+                                                    const int32_t* row_dst, const int8_t* gu, const uint8_t* gu_scale,
+                                                    const void* W1, const void* W2, const void* d_combine_buf,
+                                                    void* d_x_slots, void* dW1, void* dW2, void* workspace,
+                                                    size_t ws_bytes, void* stream);
 
 MOE_API const char* moe_status_string(moe_status_t s);
 MOE_API int moe_last_hip_error(void);
