@@ -326,6 +326,18 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
   return launch_gemm_w4a4(P, G, s);
 }
 
+// Whether the kernel for few rows takes a Linear on 8-bit integers: at most 8 rows
+// per expert, if the router spreads them evenly (the host does not see the
+// call's offsets; an expert with more than 32 takes passes of 32). Whole calls of
+// the persistent GEMM / of that kernel, us, Linear-1 and Linear-2:
+//   rows per expert (tokens)     1/4 (1)      1 (4)        4 (16)       16 (64)      32 (128)
+//   8 experts, d 4096, f 14336   60/45 68/34  120/87 70/53 185/141 89/72 188/154 89/78 172/225 97/121
+//                                1/2 (16)     2 (64)       8 (256)      16 (512)
+//   32 of 256, d 7168, f 2048    85/65 52/38  156/125 81/69 146/143 90/80 147/155 94/95
+//                                1/4 (4)      4 (64)       8 (128)      16 (256)
+//   64 of 2048, 1024             24/17 16/11  61/50 40/30  51/50 34/31  51/56 35/37
+static bool few_rows(const moe_problem_t& p) { return (int64_t)p.T * p.k <= 8 * (int64_t)p.E_global; }
+
 // One Linear of the experts on 8-bit integers (see moe_int8_linear1 /
 // moe_int8_linear2), as a launch of the persistent GEMM.
 hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const int8_t* A,
@@ -334,10 +346,8 @@ hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws,
                               hipStream_t s) {
   const int G = gemm_grid(p);
   if (G <= 0) return hipErrorInvalidDevice;
-  const hipError_t e =
-      first ? launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP, ARG_ERR_LINEAR1, s)
-            : launch_plan_rows(p, L, ws, offsets, row_src, row_dst, ARG_ERR_DISPATCH_CAP | ARG_ERR_LINEAR1, 0, s);
-  if (e != hipSuccess) return e;
+  const int keep = first ? ARG_ERR_DISPATCH_CAP : ARG_ERR_DISPATCH_CAP | ARG_ERR_LINEAR1;
+  const int mark = first ? ARG_ERR_LINEAR1 : 0;
   GemmParams P = gemm_params(p, L, ws, G, A, nullptr, row_dst, W, nullptr, W, nullptr, out, nullptr, 0);
   P.Ar = A_scale;
   P.Wc = W_scale;
@@ -346,6 +356,9 @@ hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws,
   P.a_k = p.k;
   P.trace = nullptr;
   P.mode = first ? MODE_SEP_L1 : MODE_SEP_L2;
+  if (few_rows(p)) return launch_int8_rows(P, RowsPlan{offsets, L.E_l, (int64_t)p.T * p.k, keep, mark}, G, s);
+  const hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, keep, mark, s);
+  if (e != hipSuccess) return e;
   return launch_gemm_int8(P, G, s);
 }
 

@@ -127,6 +127,15 @@ hipError_t launch_gemm_fp8(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_w4a8(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_w4a4(const GemmParams& P, int G, hipStream_t s);
 hipError_t launch_gemm_int8(const GemmParams& P, int G, hipStream_t s);
+// 8-bit integers for experts of few rows, with the plan in the same launch:
+// what the checks of plan_rows_kernel take besides P.
+struct RowsPlan {
+  const int32_t* offsets;
+  int El;
+  int64_t src_end;
+  int keep, mark;
+};
+hipError_t launch_int8_rows(const GemmParams& P, const RowsPlan& R, int G, hipStream_t s);
 hipError_t launch_gemm_checkpoint(const GemmParams& P, int G, hipStream_t s);  // Linear-1
 const void* gemm_kernel_bf16();
 

@@ -137,11 +137,11 @@ def test_linear2(name, bf16_buf, tiles):
     assert np.all(got[A:] == 5.0)
 
 
+@pytest.mark.parametrize("T", [3, 40])
 @pytest.mark.parametrize("first", [True, False])
-def test_longest_sums(first):
+def test_longest_sums(first, T):
     """K just below 2^17: sums of -128 x -128 reach 2^31 - 2^21, and of 127 x -128 the same below zero."""
     K = (1 << 17) - 128
-    T = 3
     p = moe.make_problem(T, K if first else 128, 128 if first else K, 1, 1, sched="auto")
     x = torch.full((T, K), -128, dtype=torch.int8, device="cuda")
     x[1] = 127
@@ -165,20 +165,59 @@ def test_longest_sums(first):
     assert ((got - ref[:, None]).abs() <= tol[:, None]).all()
 
 
-def test_poisoned_scales_reach_their_products_only():
-    cfg, disp, g = _setup(CASES["odd_rows"])
+@pytest.mark.parametrize("counts", [[1, 7, 8, 9], [0, 15, 16, 17], [31, 0, 32, 33], [0, 0, 64, 0], [65, 1, 0, 300]])
+@pytest.mark.parametrize("E", [4, 300])
+def test_rows_per_expert_around_the_borders(counts, E):
+    """Row counts around the passes of the kernel for few rows (E = 300: the mean says few, whatever the counts) and the
+    tiles of the other, offsets that do not start at zero, slots in any order."""
+    d, f, first = 384, 256, 3
+    A = first + sum(counts)
+    off = np.zeros(E + 1, np.int64)
+    off[:] = first + sum(counts)
+    at = sorted(np.random.default_rng(E).choice(E, 4, replace=False))
+    full = np.zeros(E, np.int64)
+    full[at] = counts
+    off = first + np.concatenate([[0], np.cumsum(full)])
+    p = moe.make_problem(A, d, f, E, 1, sched="auto")
+    g = torch.Generator().manual_seed(A)
+    (x, xs), (w, ws_) = _rand(g, A, d), _rand(g, E, 2 * f, d)
+    (h, hs), (w2, w2s) = _rand(g, A, f), _rand(g, E, d, f)
+    H = torch.full((A, f), 5.0, dtype=torch.bfloat16, device="cuda")
+    C = torch.full((A, d), 5.0, device="cuda")
+    ws, dst = moe.alloc_workspace(p), np.random.default_rng(A).permutation(A)
+    moe.int8_linear1(p, x.cuda(), xs.cuda(), None, _i32(off), w.cuda(), ws_.cuda(), H, ws)
+    moe.int8_linear2(p, h.cuda(), hs.cuda(), _i32(off), _i32(dst), w2.cuda(), w2s.cuda(), C, ws)
+    moe.check_workspace(p, ws)
+    v = moe.workspace_views(p, ws)
+    assert int(v["meta"][0]) == A and int(v["meta"][1]) == sum(-(-c // 256) for c in counts)
+    H, C = H.double().cpu().numpy(), C.double().cpu().numpy()
+    assert np.all(H[:first] == 5.0) and np.all(C[dst[:first]] == 5.0)
+    for e in at:
+        r = slice(off[e], off[e + 1])
+        gate, u = np.split(_Scaled(x, xs)[r].times(_Scaled(w, ws_)[e]), 2, axis=1)
+        ref = gate / (1 + np.exp(-gate)) * u
+        tol = 4 * U * (1.1 * np.abs(u * gate) + np.abs(ref)) + 16 * U * (1 + np.abs(gate)) * np.abs(ref)
+        assert np.all(np.abs(H[r] - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
+        ref = _Scaled(h, hs)[r].times(_Scaled(w2, w2s)[e])
+        assert np.all(np.abs(C[dst[r]] - ref) <= 4 * U * np.abs(ref) + 1e-30), e
+
+
+@pytest.mark.parametrize("name", ["odd_rows", "few_tokens"])
+def test_poisoned_scales_reach_their_products_only(name):
+    cfg, disp, g = _setup(CASES[name])
+    t, e = (7, 2) if name == "odd_rows" else (3, 1)
     x, xs = _rand(g, cfg.T, cfg.d)
     w, ws_ = _rand(g, cfg.E_local, 2 * cfg.f, cfg.d)
-    xs[7] = float("nan")              # token 7
-    x[7] = 0                          # ... as the quantiser leaves a row it cannot hold
-    ws_[2, cfg.f + 5] = float("nan")  # the up row of column 5 of local expert 2
+    xs[t] = float("nan")              # one token
+    x[t] = 0                          # ... as the quantiser leaves a row it cannot hold
+    ws_[e, cfg.f + 5] = float("nan")  # the up row of column 5 of one local expert
     p = problem_of(cfg, sched="auto")
     H = torch.zeros(cfg.cap, cfg.f, dtype=torch.bfloat16, device="cuda")
     moe.int8_linear1(p, x.cuda(), xs.cuda(), _i32(disp["row_src"], cfg.cap), _i32(disp["offsets"]), w.cuda(),
                      ws_.cuda(), H, moe.alloc_workspace(p))
     want = np.zeros((disp["A"], cfg.f), bool)
-    want[disp["row_src"] // cfg.k == 7] = True
-    want[disp["offsets"][2]:disp["offsets"][3], 5] = True
+    want[disp["row_src"] // cfg.k == t] = True
+    want[disp["offsets"][e]:disp["offsets"][e + 1], 5] = True
     np.testing.assert_array_equal(torch.isnan(H).cpu().numpy()[:disp["A"]], want)
 
 
@@ -236,22 +275,25 @@ def test_w8a8_layer_run_together():
     assert np.linalg.norm(Yref - exact) <= 0.06 * np.linalg.norm(exact)
 
 
-@pytest.mark.parametrize("bad", ["src_high", "src_negative", "dst_high", "offsets"])
-def test_device_side_checks(bad):
-    cfg, disp, g = _setup(CASES["odd_rows"])
+@pytest.mark.parametrize("name", ["odd_rows", "few_tokens"])
+@pytest.mark.parametrize("bad", ["src_high", "src_negative", "dst_high", "offsets", "not_monotone"])
+def test_device_side_checks(bad, name):
+    cfg, disp, g = _setup(CASES[name])
     p = problem_of(cfg, sched="auto")
     (x, xs), (w1, w1s) = _rand(g, cfg.T, cfg.d), _rand(g, cfg.E_local, 2 * cfg.f, cfg.d)
     (h, hs), (w2, w2s) = _rand(g, cfg.cap, cfg.f), _rand(g, cfg.E_local, cfg.d, cfg.f)
     src, dst, off = _i32(disp["row_src"], cfg.cap), _i32(disp["row_dst"], cfg.cap), _i32(disp["offsets"])
     good = src.clone(), dst.clone(), off.clone()
     if bad == "src_high":
-        src[10] = cfg.T * cfg.k
+        src[disp["A"] // 3] = cfg.T * cfg.k
     elif bad == "src_negative":
         src[disp["A"] - 1] = -1
     elif bad == "dst_high":
         dst[disp["A"] // 2] = cfg.cap
-    else:
+    elif bad == "offsets":
         off[-1] = cfg.cap + 1
+    else:
+        off[1] = off[2] + 1
     ws = moe.alloc_workspace(p)
     H = torch.full((cfg.cap, cfg.f), 5.0, dtype=torch.bfloat16, device="cuda")
     C = torch.full((cfg.cap, cfg.d), 5.0, device="cuda")
@@ -265,7 +307,7 @@ def test_device_side_checks(bad):
     for call, out in ((lambda: one(src, off), H), (lambda: two(dst, off), C)):
         call()
         torch.cuda.synchronize()
-        reached = bad == "offsets" or (bad.startswith("src")) == (out is H)
+        reached = bad in ("offsets", "not_monotone") or (bad.startswith("src")) == (out is H)
         if reached:
             with pytest.raises(moe.MoEError) as ei:
                 moe.check_workspace(p, ws)
@@ -283,9 +325,10 @@ def test_device_side_checks(bad):
     assert torch.isfinite(H).all() and not torch.all(H[:disp["A"]] == 5.0)
 
 
-def test_rows_past_the_last_are_not_looked_at():
+@pytest.mark.parametrize("name", ["odd_blocks", "empty_experts"])
+def test_rows_past_the_last_are_not_looked_at(name):
     """Indices and scales behind the last row may hold anything."""
-    cfg, disp, g = _setup(CASES["odd_blocks"])
+    cfg, disp, g = _setup(CASES[name])
     A = disp["A"]
     p = problem_of(cfg, sched="auto")
     (x, xs), (w, ws_) = _rand(g, cfg.T, cfg.d), _rand(g, cfg.E_local, 2 * cfg.f, cfg.d)
