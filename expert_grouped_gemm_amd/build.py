@@ -23,6 +23,10 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hi
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include"), "-Wall", "-Wno-unused-function"]
 
+# The SDWA peephole pass takes 200 of 280 seconds on the byte conversions in this file's 80 unrolled epilogues; without
+# it the same kernel compiles in 70.
+FILE_FLAGS = {"expert_backward_checkpoint.hip": ["-mllvm", "-amdgpu-sdwa-peephole=0"]}
+
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
     obj_dir = os.path.join(HERE, "_build")
@@ -32,7 +36,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     for src in SOURCES:
         obj = os.path.join(obj_dir, src.replace(".hip", ".o"))
         objs.append(obj)
-        cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        cmd = [HIPCC, *FLAGS, *FILE_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))

@@ -318,19 +318,17 @@ struct BwdTile {
   int cols;     // valid output columns (128 or 256)
 };
 
-// Gate and up of columns col .. col + 3 of a row.
+// Gate and up of columns col .. col + 3 of a row: the fp32 products, or the
+// checkpoint's codes (32-bit offsets: cap * 2f codes are below 2^32).
 template <int OP>
 __device__ __forceinline__ void load_gate_up(const BwdParams& P, size_t row, int col, float (&g)[4], float (&u)[4]) {
   if constexpr (OP == BWD_DACT8) {
-    const int8_t* codes = P.gu8 + row * (2 * (size_t)P.f) + col;
-    const uint8_t* scales = P.gus + row * (size_t)(P.f >> 4) + (col >> 5);
-    const int cg = *reinterpret_cast<const int*>(codes), cu = *reinterpret_cast<const int*>(codes + P.f);
-    const float sg = mxint8_step(scales[0]), su = mxint8_step(scales[P.f >> 5]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      g[i] = (float)(int8_t)(cg >> (8 * i)) * sg;
-      u[i] = (float)(int8_t)(cu >> (8 * i)) * su;
-    }
+    const uint32_t at = (uint32_t)row * (2 * (uint32_t)P.f) + (uint32_t)col;
+    const uint32_t cg = *reinterpret_cast<const uint32_t*>(P.gu8 + at);
+    const uint32_t cu = *reinterpret_cast<const uint32_t*>(P.gu8 + (at + (uint32_t)P.f));
+    const uint32_t sg = P.gus[at >> 5], su = P.gus[(at + (uint32_t)P.f) >> 5];
+    mxint8_values4(cg, mxint8_step(sg), g);
+    mxint8_values4(cu, mxint8_step(su), u);
   } else {
     const float* gu = P.GU + row * (2 * (size_t)P.f) + col;
     const float4 g4 = *reinterpret_cast<const float4*>(gu), u4 = *reinterpret_cast<const float4*>(gu + P.f);

@@ -1,6 +1,8 @@
 // 8-bit integer codecs: rows with one fp32 scale each (the operands of
 // moe_int8_linear1 / moe_int8_linear2), and OCP MXINT8 (one E8M0 scale per 32
 // consecutive elements of a row: the checkpoints of activations).
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -76,36 +78,41 @@ __device__ __forceinline__ float row_scale(float amax) {
 
 // ------------------------------------------------------ rows of 8-bit integers
 
-// One row per workgroup of NT lanes, its values in registers between the
-// maximum and the codes (CH groups of 8 per lane; a row with more is read
-// again), so that a row is read once.
-template <bool F32_IN, int NT, int CH>
-__global__ __launch_bounds__(NT) void int8_quantize_kernel(const void* __restrict__ x, int64_t rows, int64_t g,
-                                                           uint2* __restrict__ codes, float* __restrict__ scales) {
-  __shared__ uint32_t part[NT / 64];
-  const int tid = threadIdx.x;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int64_t base = r * g;
+// A row per LPR lanes, its values in registers between the maximum and the
+// codes (CH groups of 8 per lane; a row with more is read again), so that a row
+// is read once. Bound by HBM: 16384 x 14336 bf16 values 131 us for 705 MB, 5.4
+// TB/s. The fewest lanes of 16, 64, 256 and 512 whose registers hold the row
+// (bf16, us, with 16 / 64 / 256 / 512 lanes): 65536 x 128 7.7 / 22 / 63 / 136,
+// x 512 19 / 24 / 66 / 142, x 2048 - / 77 / 96 / 177, 32768 x 7168 - / - / 130 /
+// 147, 16384 x 14336 - / - / 134 / 131 (1024 lanes 192).
+template <bool F32_IN, int LPR, int CH>
+__global__ __launch_bounds__(LPR > 256 ? LPR : 256) void int8_quantize_kernel(const void* __restrict__ x, int64_t rows,
+                                                                             int64_t g, uint2* __restrict__ codes,
+                                                                             float* __restrict__ scales) {
+  constexpr int NT = LPR > 256 ? LPR : 256, RPB = NT / LPR;  // rows per workgroup
+  __shared__ uint32_t part[LPR > 64 ? NT / 64 : 1];
+  const int l = threadIdx.x % LPR;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < rows; r0 += (int64_t)gridDim.x * RPB) {
+    const int64_t r = r0 + threadIdx.x / LPR;
+    const int64_t mine = r < rows ? g : 0, base = r * g;  // groups of this lane's row
     uint32_t b[CH][8];
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int64_t c = tid + (int64_t)j * NT;
-      if (c < g) load_bits8<F32_IN>(x, base + c, b[j]);
-    }
+    for (int j = 0; j < CH; ++j)
+      if (l + j * LPR < mine) load_bits8<F32_IN>(x, base + l + j * LPR, b[j]);
 #pragma unroll
     for (int j = 0; j < CH; ++j)
-      if (tid + (int64_t)j * NT < g) m = max_magnitude(b[j], m);
-    for (int64_t c = tid + (int64_t)CH * NT; c < g; c += NT) {
+      if (l + j * LPR < mine) m = max_magnitude(b[j], m);
+    for (int64_t c = l + CH * LPR; c < mine; c += LPR) {
       uint32_t v[8];
       load_bits8<F32_IN>(x, base + c, v);
       m = max_magnitude(v, m);
     }
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-    if constexpr (NT > 64) {
+    for (int off = 1; off < (LPR < 64 ? LPR : 64); off <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+    if constexpr (LPR > 64) {
       __syncthreads();  // the last row's maxima have been read
-      if ((tid & 63) == 0) part[tid >> 6] = m;
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < NT / 64; ++i) m = max(m, part[i]);
@@ -122,16 +129,14 @@ __global__ __launch_bounds__(NT) void int8_quantize_kernel(const void* __restric
       codes[base + c] = o;
     };
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int64_t c = tid + (int64_t)j * NT;
-      if (c < g) put(c, b[j]);
-    }
-    for (int64_t c = tid + (int64_t)CH * NT; c < g; c += NT) {
+    for (int j = 0; j < CH; ++j)
+      if (l + j * LPR < mine) put(l + j * LPR, b[j]);
+    for (int64_t c = l + CH * LPR; c < mine; c += LPR) {
       uint32_t v[8];
       load_bits8<F32_IN>(x, base + c, v);
       put(c, v);
     }
-    if (tid == 0) scales[r] = bad ? __builtin_nanf("") : row_scale(amax);
+    if (l == 0 && mine) scales[r] = bad ? __builtin_nanf("") : row_scale(amax);
   }
 }
 
@@ -220,12 +225,21 @@ unsigned codec_blocks(int64_t lanes) {
 hipError_t launch_int8_quantize(const void* x, bool f32, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                                 hipStream_t s) {
   if (rows == 0) return hipSuccess;
-  const unsigned blocks = (unsigned)(rows < (1 << 20) ? rows : (1 << 20));
-  auto go = [&](auto kern, int nt) {
-    hipLaunchKernelGGL(kern, dim3(blocks), dim3(nt), 0, s, x, rows, cols / 8, reinterpret_cast<uint2*>(codes), scales);
+  auto go = [&](auto kern, int lpr) {
+    const int nt = lpr > 256 ? lpr : 256;
+    const int64_t blocks = (rows + nt / lpr - 1) / (nt / lpr);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(nt), 0, s, x, rows,
+                       cols / 8, reinterpret_cast<uint2*>(codes), scales);
   };
-  if (f32) go(int8_quantize_kernel<true, 256, 8>, 256);
-  else go(int8_quantize_kernel<false, 256, 8>, 256);
+  auto pick = [&](auto f) {
+    constexpr bool F = decltype(f)::value;
+    if (cols <= 512) go(int8_quantize_kernel<F, 16, 4>, 16);
+    else if (cols <= 2048) go(int8_quantize_kernel<F, 64, 4>, 64);
+    else if (cols <= 8192) go(int8_quantize_kernel<F, 256, 4>, 256);
+    else go(int8_quantize_kernel<F, 512, 4>, 512);
+  };
+  if (f32) pick(std::true_type{});
+  else pick(std::false_type{});
   return hipGetLastError();
 }
 

@@ -331,15 +331,24 @@ __device__ __forceinline__ float mxint8_step(uint32_t byte) {
 __device__ __forceinline__ uint32_t mxint8_code(float x, float inverse_step) {
   return __float_as_uint(__builtin_amdgcn_fmed3f(x * inverse_step, -127.0f, 127.0f) + 12582912.0f);
 }
-// Eight codes as values (each exact, in bf16 too).
+// Four codes of a word as values (each exact, in bf16 too): a code + 128 is the
+// byte with its top bit turned, which one instruction converts.
+__device__ __forceinline__ void mxint8_values4(uint32_t c, float step, float (&v)[4]) {
+  c ^= 0x80808080u;
+  v[0] = ((float)(c & 0xFFu) - 128.0f) * step;
+  v[1] = ((float)((c >> 8) & 0xFFu) - 128.0f) * step;
+  v[2] = ((float)((c >> 16) & 0xFFu) - 128.0f) * step;
+  v[3] = ((float)(c >> 24) - 128.0f) * step;
+}
+// Eight codes.
 __device__ __forceinline__ void mxint8_values8(uint2 c, float step, float (&v)[8]) {
-  const int w[2] = {(int)c.x, (int)c.y};
+  float lo[4], hi[4];
+  mxint8_values4(c.x, step, lo);
+  mxint8_values4(c.y, step, hi);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[4 * i] = (float)(int8_t)w[i] * step;
-    v[4 * i + 1] = (float)(int8_t)(w[i] >> 8) * step;
-    v[4 * i + 2] = (float)(int8_t)(w[i] >> 16) * step;
-    v[4 * i + 3] = (float)(w[i] >> 24) * step;
+  for (int i = 0; i < 4; ++i) {
+    v[i] = lo[i];
+    v[4 + i] = hi[i];
   }
 }
 
