@@ -33,8 +33,6 @@ hipError_t launch_bands(const BwdParams& P, int G, hipStream_t s) {
 
 }  // namespace
 
-bool long_experts(const moe_problem_t& p) { return (int64_t)p.T * p.k > (int64_t)kShortRows * p.E_global; }
-
 hipError_t launch_backward_dx(const BwdParams& P, int G, hipStream_t s) { return launch_bands<BWD_DX>(P, G, s); }
 
 hipError_t launch_order_rows(const BwdParams& P, hipStream_t s) {

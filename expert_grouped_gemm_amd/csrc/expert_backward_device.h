@@ -27,19 +27,18 @@
 // Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
 // without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
 // but for the weight gradients, whose tiles of two to five stages are half setup
-// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DX 386 (4.9), DW2 291 (3.2), DW1 590
-// (3.2). 16384 rows of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy
-// 59% of the time at the clock the chip holds under them, and the loads and LDS
-// reads that do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the
-// epilogue's 3.3 GB), DX 3408 (1129), DW2 1906 (1009), DW1 3751 (1026).
-// These last two (WAVES = 8) spill 16 registers, output row numbers of their
-// epilogue that one loader role reloads between its stores; no accumulator and
-// nothing of a K loop is spilled, and no other kernel here spills any.
+// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DACT8 205 (from a checkpoint, 5.1
+// with its codes and results), DX 386 (4.9), DW2 255 (3.7), DW1 502 (3.7). 16384 rows
+// of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy 55-59% of the
+// time at the clock the chip holds under them, and the loads and LDS reads that
+// do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the epilogue's 3.3
+// GB), DACT8 2210 (870), DX 3408 (1129), DW2 1680 (1145), DW1 3400 (1132).
+// No kernel here spills a register.
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
 // fragments read across the barrier (20% slower) and every wavefront loading
-// (6%), both while the loads still went through the builtin (see dma16); the
-// next weight-gradient tile's loads issued before the stores of the last, and
-// DACT's gate and up values all fetched ahead of its stores (registers spilled).
+// (6%), both on eight wavefronts and while the loads still went through the
+// builtin (see dma16); DACT's gate and up values all fetched ahead of its stores,
+// in fp32 or as codes (registers spilled).
 #pragma once
 
 #include "gemm_device.h"
@@ -57,8 +56,8 @@ struct BwdParams {
   uint16_t* dxs;             // [cap, d] by slot
   uint16_t* dW1;
   uint16_t* dW2;
-  uint16_t* Xp;              // long experts: the token rows and the output gradients in expert order
-  uint16_t* dOp;             // [cap, d] each
+  uint16_t* Xp;              // the token rows (MXINT8 tokens, long experts) and the output gradients
+  uint16_t* dOp;             // (long experts) in expert order, [cap, d] each
   const int32_t* row_src;    // or null
   const int32_t* row_dst;
   const int32_t* offsets;
@@ -72,7 +71,8 @@ struct BwdParams {
   int k, d, f, El, group_m;
 };
 
-// Rows per expert, if the router spreads them evenly, above kShortRows.
+// Whether the weight gradients take the kernel for long experts (see
+// expert_backward_weights.hip), which reads ordered copies of the rows.
 bool long_experts(const moe_problem_t& p);
 
 // The parameters of a call whose intermediates lie at B in its workspace.
@@ -115,18 +115,6 @@ __host__ __device__ constexpr int bwd_ring(int PB, int QB) {
   const int s = kGemmLds / stage_bytes_of(PB + QB);
   return s > 6 ? 6 : s;
 }
-
-// Rows per expert up to which weight_backward_short_kernel runs. Whole calls
-// with it / with the other kernel and its copies, us:
-//   rows per expert              128          256          512         1024          2048
-//   32 experts, d 7168, f 2048   1812 / 1932  3340 / 3335  5257 / 5090  9179 / 8623  17264 / 15646
-//   8 of 4096, 14336                          3444 / 3401  5458 / 5182  9294 / 8576  17291 / 15308
-//   16 of 2048, 1024              183 / 203    279 / 295    453 / 458    767 / 763    1402 / 1359
-// They cross between 256 and 640 rows; at 512 the two differ by at most 5%. The
-// rows are the router's mean, T k / E_global, as the host does not see the call's
-// offsets: a share that holds the favoured experts may take the short kernel for
-// long ones (4 of 64 experts, a Zipf router, 8192 tokens: 2119 / 1923).
-constexpr int kShortRows = 512;
 
 // One operand of a tile. KC: `valid` rows (the non-K dimension) of pitch
 // bytes; KS: `valid` K rows, of which the tile takes the columns from base on
@@ -225,66 +213,6 @@ struct BandLoads {
     const uint8_t* b0 = base + (size_t)kt * (kBK * 2);
 #pragma unroll
     for (int j = 0; j < NI; ++j) dma16<false>(b0, off[j], st + (4 * j + lw) * 1024);
-  }
-};
-
-// An expert's rows as K (KS), BK of them a stage, perhaps through idx. Lane kk
-// holds the offset of K row kk of a stage for all lanes; rows past the last
-// re-read it (the stage's LDS rows are zeroed). Offsets through idx fit 32 bits
-// (the problem limits keep T * d and cap * d below 2^31 elements) and are
-// fetched ahead: those of a tile's first S stages together, a later stage's
-// when the stage before it is issued. Without idx they count from the stage's
-// first row.
-// IDX: the rows may be looked up (otherwise they stand in expert order).
-template <int BLOCKS, int BK, int S, bool IDX>
-struct RowLoads {
-  static constexpr int CPR = BLOCKS * 4, RPI = 64 / CPR, NI = BK * BLOCKS / 64;
-  const uint8_t* base;
-  uint32_t pitch, lane_off, ahead[S];
-  const int32_t* idx;
-  int div, valid;
-
-  __device__ __forceinline__ uint32_t look_up(int kt, int lane) const {
-    return (uint32_t)(idx[min(kt * BK + (lane & (BK - 1)), valid - 1)] / div) * pitch;
-  }
-  __device__ __forceinline__ void init(const Side& s, int lw, int lane) {
-    base = s.base;
-    pitch = s.pitch;
-    idx = IDX ? s.idx : nullptr;
-    div = s.div;
-    valid = s.valid;
-    const int kk = lw * RPI + lane / CPR;
-    lane_off = (((lane % CPR) ^ ks_swizzle(kk)) & (s.chunks - 1)) << 4;
-    if (idx && valid > 0) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) ahead[i] = look_up(i, lane);
-    }
-  }
-  __device__ __forceinline__ void issue_rows(int kt, uint32_t rows, lds_t* st, int lw, int lane) {
-    const int kk = lw * RPI + lane / CPR, left = valid - kt * BK;
-    const uint8_t* b0 = idx ? base : base + (size_t)kt * BK * pitch;
-    if (!idx && left >= BK) {
-      const uint32_t off = kk * pitch + lane_off;
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-        dma16<false>(b0 + (size_t)(4 * j * RPI) * pitch, off, st + (4 * j + lw) * 1024);
-      return;
-    }
-    if (!idx) rows = min(lane & (BK - 1), left - 1) * pitch;
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-      dma16<false>(b0, (uint32_t)__shfl((int)rows, 4 * j * RPI + kk, 64) + lane_off, st + (4 * j + lw) * 1024);
-  }
-  // stage kt < S, of the tile's first ones
-  __device__ __forceinline__ void issue_first(int kt, lds_t* st, int lw, int lane) {
-    issue_rows(kt, ahead[kt], st, lw, lane);
-    if (kt == S - 1 && idx) ahead[0] = look_up(S, lane);
-  }
-  // a later stage
-  __device__ __forceinline__ void issue(int kt, lds_t* st, int lw, int lane) {
-    const uint32_t rows = ahead[0];
-    if (idx && (kt + 1) * BK < valid) ahead[0] = look_up(kt + 1, lane);
-    issue_rows(kt, rows, st, lw, lane);
   }
 };
 
@@ -592,124 +520,12 @@ __device__ __forceinline__ void take_rows(BwdTile& t, int first, int count) {
   else t.Q.base += (size_t)first * t.Q.pitch;
 }
 
-// Tile (m, n) of an expert's weight gradient, TM rows high. IDX: the rows of X
-// and dO are looked up; otherwise they are read from their ordered copies.
-template <int OP, bool IDX>
-__device__ __forceinline__ BwdTile weight_tile(const BwdParams& P, int e, int m, int n, int TM) {
-  BwdTile t;
-  t.e = e;
-  const int r0 = P.offsets[e], cnt = P.offsets[e + 1] - r0;
-  const int M = OP == BWD_DW2 ? P.d : 2 * P.f, N = OP == BWD_DW2 ? P.f : P.d;
-  t.row0 = m * TM;
-  t.rows = min(TM, M - t.row0);
-  t.col0 = n * 256;
-  t.cols = min(256, N - t.col0);
-  const uint32_t db = (uint32_t)P.d * 2, fb = (uint32_t)P.f * 2;
-  if constexpr (OP == BWD_DW2) {
-    t.P = Side{reinterpret_cast<const uint8_t*>(P.act) + (size_t)r0 * fb + (size_t)t.col0 * 2, fb, cnt, t.cols / 8,
-               nullptr, 1};
-    t.Q = IDX ? Side{P.dO + (size_t)t.row0 * 2, db, cnt, t.rows / 8, P.row_dst + r0, 1}
-              : Side{reinterpret_cast<const uint8_t*>(P.dOp) + (size_t)r0 * db + (size_t)t.row0 * 2, db, cnt,
-                     t.rows / 8, nullptr, 1};
-  } else {
-    const uint8_t* rows = IDX || !P.row_src ? P.X : reinterpret_cast<const uint8_t*>(P.Xp);
-    t.P = IDX && P.row_src ? Side{P.X + (size_t)t.col0 * 2, db, cnt, t.cols / 8, P.row_src + r0, P.k}
-                           : Side{rows + (size_t)r0 * db + (size_t)t.col0 * 2, db, cnt, t.cols / 8, nullptr, 1};
-    t.Q = Side{reinterpret_cast<const uint8_t*>(P.dH) + (size_t)r0 * (2 * fb) + (size_t)t.row0 * 2, 2 * fb, cnt,
-               t.rows / 8, nullptr, 1};
-  }
-  return t;
-}
-
-// DW1 or DW2: a workgroup's tiles, one after the other.
-// WAVES = 8: 256 x 256 tiles, a ring of two stages of 64 K rows, one workgroup
-// per CU, the last four wavefronts load. WAVES = 4: 128 x 256 tiles, three
-// stages of 32 K rows, two workgroups per CU (72 KiB of LDS each), every
-// wavefront loads: for experts of few rows, whose tiles are a few stages long
-// and otherwise setup, waits and stores, which the two workgroups overlap.
-// A tile starts with the whole ring in flight; from step 1 on, each step
-// refills the slot of the step before it.
-template <int OP, int WAVES, bool LOADER, int WQ>
-__device__ __forceinline__ void weight_tiles_body(const BwdParams& P, lds_t* lds, int lid, int G) {
-  constexpr int QB = WAVES, BK = WAVES == 8 ? 64 : 32, S = WAVES == 8 ? 2 : 3, NW = WAVES / 4, TM = QB * 32;
-  constexpr int SB = (8 + QB) * 64 * BK;  // stage bytes: 64 of each block per K row
-  int tid = threadIdx.x;
-  asm volatile("" : "+v"(tid));
-  const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), wp = w / NW, lw = w - (WAVES - 4);
-  const int rows_all = OP == BWD_DW2 ? P.d : 2 * P.f, cols_all = OP == BWD_DW2 ? P.f : P.d;
-  const int M = (rows_all + TM - 1) / TM, N = (cols_all + 255) / 256;
-  const int64_t total = (int64_t)P.El * M * N;
-  typedef RowLoads<8, BK, S, WAVES == 4> LoadsP;
-  typedef RowLoads<QB, BK, S, WAVES == 4> LoadsQ;
-  constexpr int LD = LoadsP::NI + LoadsQ::NI;
-  for (int64_t i = lid; i < total; i += G) {
-    const int e = (int)(i / (M * N));
-    int m, n;
-    raster((int)(i - (int64_t)e * M * N), M, N, P.group_m, m, n);
-    const BwdTile t = weight_tile<OP, WAVES == 4>(P, e, m, n, TM);
-    const int KT = (t.P.valid + BK - 1) / BK;
-    LoadsP lp;
-    LoadsQ lq;
-    if constexpr (LOADER) {
-      lp.init(t.P, lw, lane);
-      lq.init(t.Q, lw, lane);
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (s < KT) {
-          lp.issue_first(s, lds + s * SB, lw, lane);
-          lq.issue_first(s, lds + s * SB + 8 * 64 * BK, lw, lane);
-        }
-    }
-    f32x16 acc[4][2];
-    clear_acc(acc);
-    int rd = 0, wr = S - 1;
-    for (int kt = 0; kt < KT; ++kt) {
-      if constexpr (LOADER) wait_stages<LD, S - 1>(min(KT - 1, kt == 0 ? S - 1 : kt + S - 2) - kt);
-      lds_barrier();
-      lds_t* st = lds + rd * SB;
-      // K rows past the expert's last: zero on both sides
-      const int left = t.P.valid - kt * BK;
-      if (left < BK) {
-        for (int c = left * 32 + tid; c < BK * 32; c += WAVES * 64) *(lds_i32x4*)(st + c * 16) = i32x4{0, 0, 0, 0};
-        for (int c = left * (QB * 4) + tid; c < BK * (QB * 4); c += WAVES * 64)
-          *(lds_i32x4*)(st + 8 * 64 * BK + c * 16) = i32x4{0, 0, 0, 0};
-        lds_barrier();
-      }
-      bwd_stage<true, true, 8, QB, 4, BK, NW>(st, WQ, wp, lane, acc, [&]() {
-        if constexpr (LOADER) {
-          if (kt > 0 && kt + S - 1 < KT) {
-            lp.issue(kt + S - 1, lds + wr * SB, lw, lane);
-            lq.issue(kt + S - 1, lds + wr * SB + 8 * 64 * BK, lw, lane);
-          }
-        }
-      });
-      rd = rd + 1 == S ? 0 : rd + 1;
-      wr = wr + 1 == S ? 0 : wr + 1;
-    }
-    lds_barrier();  // the ring is free
-    if (wp * 64 < t.cols) {
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int m0 = (WQ + NW * a) * 32;
-        if (m0 < t.rows) store_block<OP, 2>(P, t, lds + w * 4096, acc[a], m0, wp * 64, 0, lane);
-      }
-    }
-    lds_barrier();  // ... for the next tile's loads
-  }
-}
-
 // Workgroup b's place in the tile order: consecutive places on one XCD
 // (workgroups are dealt to the 8 XCDs in turn).
 __device__ __forceinline__ int place(int b, int G) { return G % 8 == 0 ? (b % 8) * (G / 8) + b / 8 : b; }
 
-// The weight gradients of experts with few rows.
-template <int OP>
-__global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * 12 * 64 * 32];
-  if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
-  weight_tiles_body<OP, 4, true, 0>(P, (lds_t*)smem, place(blockIdx.x, gridDim.x), gridDim.x);
-}
-
+// GU, DACT and DX. (DW2 and DW1, of other tiles, are specialised in
+// expert_backward_weights.hip.)
 template <int OP>
 __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kGemmLds];
@@ -717,46 +533,35 @@ __global__ __launch_bounds__(kBwdThreads, 1) void expert_backward_kernel(BwdPara
   const int G = gridDim.x, lid = place(blockIdx.x, G);
   // rejected row indices or offsets: nothing is computed
   if (P.meta[META_ARG_ERR] & ARG_ERR_PLAN) return;
-  if constexpr (OP <= BWD_DX || OP == BWD_DACT8) {
-    const int nb = P.meta[META_P];
-    const int width = OP == BWD_GU ? 2 * P.f : is_dact(OP) ? P.f : P.d;
-    const int N = (width + 255) / 256, total = nb * N, cut = total / G * G;
-    // Whole rounds of 256-column tiles, then the rest as halves. Where even the
-    // halves leave workgroups idle, they are cut along the band's rows too, in
-    // two or four: a smaller stage takes less time and makes a deeper ring. Whole
-    // calls without cuts / with two / with up to four, us: one expert of 274 rows,
-    // d = 3584, f = 1024 180 / 132 / 115; of 128 rows, 2048, 1408 114 / 113 / 103; of
-    // 256 rows, 4096, 4096 331 / 240 / 228; 4 experts of 256 rows, 1024, 512
-    // 114 / 91 / 83.
-    int cuts = 1;
-    while (cuts < 4 && 4 * cuts * (total - cut) <= G) cuts *= 2;
-    for (int i = lid; i < cut + 2 * cuts * (total - cut); i += G) {
-      const bool wide = i < cut;
-      int p, n;
-      raster(wide ? i : cut + (i - cut) / (2 * cuts), nb, N, P.group_m, p, n);
-      if (!wide) n = 2 * n + ((i - cut) & 1);
-      BwdTile t = band_tile<OP>(P, p, n, wide ? 256 : 128);
-      if (!wide) take_rows(t, (((i - cut) >> 1) & (cuts - 1)) * (kBM / cuts), kBM / cuts);
-      if (t.cols <= 0 || t.rows <= 0) continue;
-      // weights of an expert with one band are read once per launch (see
-      // streams_once)
-      const bool once = (P.band_expert[p] & kBandSingle) != 0;
-      if (wide) {
-        if (once) run_band_tile<OP, 8, true>(P, t, lds);
-        else run_band_tile<OP, 8, false>(P, t, lds);
-      } else {
-        if (once) run_band_tile<OP, 4, true>(P, t, lds);
-        else run_band_tile<OP, 4, false>(P, t, lds);
-      }
-    }
-  } else {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (w >= 8 - kLoaders) {
-      if (w & 1) weight_tiles_body<OP, 8, true, 1>(P, lds, lid, G);
-      else weight_tiles_body<OP, 8, true, 0>(P, lds, lid, G);
+  const int nb = P.meta[META_P];
+  const int width = OP == BWD_GU ? 2 * P.f : is_dact(OP) ? P.f : P.d;
+  const int N = (width + 255) / 256, total = nb * N, cut = total / G * G;
+  // Whole rounds of 256-column tiles, then the rest as halves. Where even the
+  // halves leave workgroups idle, they are cut along the band's rows too, in
+  // two or four: a smaller stage takes less time and makes a deeper ring. Whole
+  // calls without cuts / with two / with up to four, us: one expert of 274 rows,
+  // d = 3584, f = 1024 180 / 132 / 115; of 128 rows, 2048, 1408 114 / 113 / 103; of
+  // 256 rows, 4096, 4096 331 / 240 / 228; 4 experts of 256 rows, 1024, 512
+  // 114 / 91 / 83.
+  int cuts = 1;
+  while (cuts < 4 && 4 * cuts * (total - cut) <= G) cuts *= 2;
+  for (int i = lid; i < cut + 2 * cuts * (total - cut); i += G) {
+    const bool wide = i < cut;
+    int p, n;
+    raster(wide ? i : cut + (i - cut) / (2 * cuts), nb, N, P.group_m, p, n);
+    if (!wide) n = 2 * n + ((i - cut) & 1);
+    BwdTile t = band_tile<OP>(P, p, n, wide ? 256 : 128);
+    if (!wide) take_rows(t, (((i - cut) >> 1) & (cuts - 1)) * (kBM / cuts), kBM / cuts);
+    if (t.cols <= 0 || t.rows <= 0) continue;
+    // weights of an expert with one band are read once per launch (see
+    // streams_once)
+    const bool once = (P.band_expert[p] & kBandSingle) != 0;
+    if (wide) {
+      if (once) run_band_tile<OP, 8, true>(P, t, lds);
+      else run_band_tile<OP, 8, false>(P, t, lds);
     } else {
-      if (w & 1) weight_tiles_body<OP, 8, false, 1>(P, lds, lid, G);
-      else weight_tiles_body<OP, 8, false, 0>(P, lds, lid, G);
+      if (once) run_band_tile<OP, 4, true>(P, t, lds);
+      else run_band_tile<OP, 4, false>(P, t, lds);
     }
   }
 }
