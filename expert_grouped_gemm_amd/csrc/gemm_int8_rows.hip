@@ -155,10 +155,11 @@ __device__ __forceinline__ bool plan_few_rows(const RowsPlan& R, const GemmParam
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const int e = j * 64 + lane;
-    const int rows = e < R.El ? R.offsets[e + 1] - R.offsets[e] : 0;
-    if (rows < 0) bits |= ARG_ERR_OFFSETS;
-    has[j] = __ballot(rows > 0);
-    bands += (max(rows, 0) + kBM - 1) / kBM;
+    // compared, not subtracted: two offsets far apart differ by more than 32 bits hold
+    const int lo = e < R.El ? R.offsets[e] : 0, hi = e < R.El ? R.offsets[e + 1] : 0;
+    if (hi < lo) bits |= ARG_ERR_OFFSETS;
+    has[j] = __ballot(hi > lo);
+    if (hi > lo) bands += (int)(((int64_t)hi - lo + kBM - 1) / kBM);
   }
   const int r_end = min(P.cap, last);
   for (int r = max(0, first) + tid; r < r_end; r += kRowsWaves * 64) {

@@ -276,7 +276,7 @@ def test_w8a8_layer_run_together():
 
 
 @pytest.mark.parametrize("name", ["odd_rows", "few_tokens"])
-@pytest.mark.parametrize("bad", ["src_high", "src_negative", "dst_high", "offsets", "not_monotone"])
+@pytest.mark.parametrize("bad", ["src_high", "src_negative", "dst_high", "offsets", "not_monotone", "far_apart"])
 def test_device_side_checks(bad, name):
     cfg, disp, g = _setup(CASES[name])
     p = problem_of(cfg, sched="auto")
@@ -292,6 +292,9 @@ def test_device_side_checks(bad, name):
         dst[disp["A"] // 2] = cfg.cap
     elif bad == "offsets":
         off[-1] = cfg.cap + 1
+    elif bad == "far_apart":  # differences that 32 bits do not hold come out small and not negative
+        off[:] = 0
+        off[1], off[2], off[3] = 2 ** 31 - 1, -2 ** 31, -1
     else:
         off[1] = off[2] + 1
     ws = moe.alloc_workspace(p)
@@ -307,7 +310,7 @@ def test_device_side_checks(bad, name):
     for call, out in ((lambda: one(src, off), H), (lambda: two(dst, off), C)):
         call()
         torch.cuda.synchronize()
-        reached = bad in ("offsets", "not_monotone") or (bad.startswith("src")) == (out is H)
+        reached = bad in ("offsets", "not_monotone", "far_apart") or (bad.startswith("src")) == (out is H)
         if reached:
             with pytest.raises(moe.MoEError) as ei:
                 moe.check_workspace(p, ws)
