@@ -336,7 +336,12 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
 //   32 of 256, d 7168, f 2048    85/65 52/38  156/125 81/69 146/143 90/80 147/155 94/95
 //                                1/4 (4)      4 (64)       8 (128)      16 (256)
 //   64 of 2048, 1024             24/17 16/11  61/50 40/30  51/50 34/31  51/56 35/37
-static bool few_rows(const moe_problem_t& p) { return (int64_t)p.T * p.k <= 8 * (int64_t)p.E_global; }
+// A padded layout (its own row_capacity) is the persistent GEMM's: its rows may be
+// many more than the router's.
+static bool few_rows(const moe_problem_t& p) {
+  return (int64_t)p.T * p.k <= 8 * (int64_t)p.E_global &&
+         row_capacity(p) == (int64_t)p.T * (p.k < p.e_end - p.e_begin ? p.k : p.e_end - p.e_begin);
+}
 
 // One Linear of the experts on 8-bit integers (see moe_int8_linear1 /
 // moe_int8_linear2), as a launch of the persistent GEMM.

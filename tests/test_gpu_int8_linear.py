@@ -328,6 +328,24 @@ def test_device_side_checks(bad, name):
     assert torch.isfinite(H).all() and not torch.all(H[:disp["A"]] == 5.0)
 
 
+def test_padded_layout():
+    """A row capacity of its own (the owner-aligned layout) on few tokens: every row of the padded experts."""
+    T, E, k, d, f, cap = 4, 4, 2, 256, 128, 700
+    off = np.array([0, 0, 300, 300, 700])
+    p = moe.make_problem(T, d, f, E, k, sched="auto", row_capacity=cap)
+    g = torch.Generator().manual_seed(1)
+    (x, xs), (w, ws_) = _rand(g, cap, d), _rand(g, E, 2 * f, d)
+    H, ws = torch.zeros(cap, f, dtype=torch.bfloat16, device="cuda"), moe.alloc_workspace(p)
+    moe.int8_linear1(p, x.cuda(), xs.cuda(), None, _i32(off), w.cuda(), ws_.cuda(), H, ws)
+    moe.check_workspace(p, ws)
+    for e in (1, 3):
+        r = slice(off[e], off[e + 1])
+        gate, u = np.split(_Scaled(x, xs)[r].times(_Scaled(w, ws_)[e]), 2, axis=1)
+        ref = gate / (1 + np.exp(-gate)) * u
+        tol = 4 * U * (1.1 * np.abs(u * gate) + np.abs(ref)) + 16 * U * (1 + np.abs(gate)) * np.abs(ref)
+        assert np.all(np.abs(H[r].double().cpu().numpy() - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
+
+
 @pytest.mark.parametrize("name", ["odd_blocks", "empty_experts"])
 def test_rows_past_the_last_are_not_looked_at(name):
     """Indices and scales behind the last row may hold anything."""
