@@ -478,6 +478,47 @@ def test_grid_changes_no_bit():
             assert torch.equal(a, b), grid
 
 
+def test_tile_trace_of_the_forward():
+    """Every tile of both launches is recorded, Linear-1's before Linear-2's."""
+    cfg, inp, disp, _ = _setup(CASES["segments"])
+    p = problem_of(cfg, sched="auto", trace=True, tiles="narrow")
+    (gu, gus), C, ws = _codes(cfg.cap, 2 * cfg.f), torch.zeros(cfg.cap, cfg.d, device="cuda"), moe.alloc_workspace(p)
+    moe.expert_forward_checkpoint(p, inp["X"].cuda(), _i32(disp["row_src"], cfg.cap), _i32(disp["offsets"]),
+                                  _i32(disp["row_dst"], cfg.cap), inp["W1"].cuda(), inp["W2"].cuda(), gu, gus, C, ws)
+    torch.cuda.synchronize()
+    tr = moe.tile_trace(p, ws)
+    bands = int(np.sum((disp["counts"] + 255) // 256))
+    assert np.sum(tr["kind"] == 1) == bands * (cfg.f // 64) and np.sum(tr["kind"] == 2) == bands * (cfg.d // 128)
+    assert tr["t_end"][tr["kind"] == 1].max() <= tr["t_start"][tr["kind"] == 2].min()
+
+
+def test_a_poisoned_block_of_the_checkpoint():
+    """A NaN scale byte: the row's gradient and its expert's weight gradients are NaN, nothing else."""
+    cfg, inp, disp, dO = _setup(CASES["odd_tokens"])
+    A, off = disp["A"], disp["offsets"]
+    gu, gus, _ = _gate_up(cfg, A)
+    e = int(np.argmax(disp["counts"]))
+    r = int(off[e])
+    gus[r, 0] = 255
+    gu[r, :32] = 0
+    p = problem_of(cfg, sched="auto")
+    out = _outputs(cfg)
+    moe.expert_backward_checkpoint(p, inp["X"].cuda(), None, _i32(disp["row_src"], cfg.cap), _i32(off),
+                                   _i32(disp["row_dst"], cfg.cap), gu, gus, inp["W1"].cuda(), inp["W2"].cuda(),
+                                   dO.cuda(), *out, moe.alloc_checkpoint_workspace(p))
+    dxs, dW1, dW2 = (t.cpu() for t in out)
+    bad = torch.zeros(cfg.cap, dtype=torch.bool)
+    bad[disp["row_dst"][r]] = True
+    assert torch.equal(torch.isnan(dxs).all(1), bad) and torch.equal(torch.isnan(dxs).any(1), bad)
+    for i in range(cfg.E_local):
+        nan1, nan2 = torch.isnan(dW1[i]), torch.isnan(dW2[i])
+        if i != e:
+            assert not nan1.any() and not nan2.any()
+        else:  # gate columns 0 .. 31: their a, dg and du
+            assert nan1[:32].all() and nan1[cfg.f:cfg.f + 32].all() and nan2[:, :32].all()
+            assert not nan1[32:cfg.f].any() and not nan1[cfg.f + 32:].any() and not nan2[:, 32:].any()
+
+
 def test_refused_by_the_binding():
     cfg, inp, disp, dO = _setup(CASES["odd_tokens"])
     p = problem_of(cfg, sched="auto")
