@@ -346,6 +346,46 @@ def test_padded_layout():
         assert np.all(np.abs(H[r].double().cpu().numpy() - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
 
 
+@pytest.mark.parametrize("E", [8, 1024])
+def test_a_problem_of_any_type_and_schedule(E):
+    """The Linears take their operands' type from the call: what the problem names for the layer's own, its schedule and
+    its segments do not matter. 1024 local experts are the most there are."""
+    T, d, f, k = 128, 256, 128, 2
+    g = torch.Generator().manual_seed(E)
+    (x, xs), (w, ws_) = _rand(g, T, d), _rand(g, E, 2 * f, d)
+    (h, hs), (w2, w2s) = _rand(g, T * k, f), _rand(g, E, d, f)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)])
+    order = torch.argsort(idx.flatten(), stable=True)
+    off = _i32(np.concatenate([[0], np.cumsum(np.bincount(idx.flatten().numpy(), minlength=E))]))
+    src, dst = order.to(torch.int32).cuda(), torch.randperm(T * k, generator=g).to(torch.int32).cuda()
+    x, xs, w, ws_, h, hs, w2, w2s = (t.cuda() for t in (x, xs, w, ws_, h, hs, w2, w2s))
+    outs = []
+    for kw in (dict(), dict(dtype="fp8_e4m3", sched="interleaved"), dict(dtype="w4a8_mxfp4", sched="separate", num_segments=4),
+               dict(sched="expert_wave", trace=True), dict(dtype="fp8_e4m3", keep_h_f32=True, band_major=True)):
+        p = moe.make_problem(T, d, f, E, k, **dict(dict(sched="auto"), **kw))
+        H, C = torch.full((T * k, f), 5.0, dtype=torch.bfloat16, device="cuda"), torch.zeros(T * k, d, device="cuda")
+        wsp = moe.alloc_workspace(p)
+        moe.int8_linear1(p, x, xs, src, off, w, ws_, H, wsp)
+        moe.int8_linear2(p, h, hs, off, dst, w2, w2s, C, wsp)
+        moe.check_workspace(p, wsp)
+        outs.append((H, C))
+    for H, C in outs[1:]:
+        assert torch.equal(H, outs[0][0]) and torch.equal(C, outs[0][1])
+    H, C = (t.double().cpu().numpy() for t in outs[0])
+    o = off.cpu().numpy()
+    X, W, Hq, W2 = _Scaled(x.cpu(), xs.cpu()), _Scaled(w.cpu(), ws_.cpu()), _Scaled(h.cpu(), hs.cpu()), _Scaled(w2.cpu(), w2s.cpu())
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        if o[e] == o[e + 1]:
+            continue
+        gate, u = np.split(X[src[r].cpu().numpy() // k].times(W[e]), 2, axis=1)
+        ref = gate / (1 + np.exp(-gate)) * u
+        tol = 4 * U * (1.1 * np.abs(u * gate) + np.abs(ref)) + 16 * U * (1 + np.abs(gate)) * np.abs(ref)
+        assert np.all(np.abs(H[r] - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
+        ref = Hq[r].times(W2[e])
+        assert np.all(np.abs(C[dst[r].cpu().numpy()] - ref) <= 4 * U * np.abs(ref)), e
+
+
 @pytest.mark.parametrize("name", ["odd_blocks", "empty_experts"])
 def test_rows_past_the_last_are_not_looked_at(name):
     """Indices and scales behind the last row may hold anything."""
