@@ -246,23 +246,13 @@ struct BwdTile {
   int cols;     // valid output columns (128 or 256)
 };
 
-// Gate and up of columns col .. col + 3 of a row: the fp32 products, or the
-// checkpoint's codes (32-bit offsets: cap * 2f codes are below 2^32).
-template <int OP>
-__device__ __forceinline__ void load_gate_up(const BwdParams& P, size_t row, int col, float (&g)[4], float (&u)[4]) {
-  if constexpr (OP == BWD_DACT8) {
-    const uint32_t at = (uint32_t)row * (2 * (uint32_t)P.f) + (uint32_t)col;
-    const uint32_t cg = *reinterpret_cast<const uint32_t*>(P.gu8 + at);
-    const uint32_t cu = *reinterpret_cast<const uint32_t*>(P.gu8 + (at + (uint32_t)P.f));
-    const uint32_t sg = P.gus[at >> 5], su = P.gus[(at + (uint32_t)P.f) >> 5];
-    mxint8_values4(cg, mxint8_step(sg), g);
-    mxint8_values4(cu, mxint8_step(su), u);
-  } else {
-    const float* gu = P.GU + row * (2 * (size_t)P.f) + col;
-    const float4 g4 = *reinterpret_cast<const float4*>(gu), u4 = *reinterpret_cast<const float4*>(gu + P.f);
-    g[0] = g4.x; g[1] = g4.y; g[2] = g4.z; g[3] = g4.w;
-    u[0] = u4.x; u[1] = u4.y; u[2] = u4.z; u[3] = u4.w;
-  }
+// dh and a of one element from its gate, up and da.
+__device__ __forceinline__ void swiglu_grad(float da, float g, float u, float& a, float& dg, float& du) {
+  const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+  const float gs = g * s;
+  a = gs * u;
+  du = da * gs;
+  dg = da * u * (s + gs * (1.0f - s));
 }
 
 // The results of one 32-row block of a wavefront (its NB * 32 columns), through
@@ -275,7 +265,7 @@ template <int OP, int NB>
 __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t, lds_t* wl, const f32x16 (&acc)[NB],
                                             int m0, int c0, int dst, int lane) {
   const int lr = lane & 31, hi = lane >> 5;
-  if constexpr (OP == BWD_GU || is_dact(OP)) {
+  if constexpr (OP == BWD_GU || OP == BWD_DACT) {
     constexpr int C = 8 * NB;  // 16-byte chunks of a row (fp32), swizzled by row
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -295,17 +285,12 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
       if constexpr (OP == BWD_GU) {
         *reinterpret_cast<float4*>(P.GU + row * (2 * (size_t)P.f) + col) = make_float4(v[0], v[1], v[2], v[3]);
       } else {
-        float g[4], u[4];
-        load_gate_up<OP>(P, row, col, g, u);
+        const float* gu = P.GU + row * (2 * (size_t)P.f) + col;
+        const float4 g4 = *reinterpret_cast<const float4*>(gu), u4 = *reinterpret_cast<const float4*>(gu + P.f);
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
         float a[4], dg[4], du[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g[i] * -1.4426950408889634f));
-          const float gs = g[i] * s;
-          a[i] = gs * u[i];
-          du[i] = v[i] * gs;
-          dg[i] = v[i] * u[i] * (s + gs * (1.0f - s));
-        }
+        for (int i = 0; i < 4; ++i) swiglu_grad(v[i], g[i], u[i], a[i], dg[i], du[i]);
         *reinterpret_cast<uint2*>(P.act + row * P.f + col) = make_uint2(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]));
         uint16_t* dh = P.dH + row * (2 * (size_t)P.f) + col;
         *reinterpret_cast<uint2*>(dh) = make_uint2(pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3]));
@@ -339,6 +324,74 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
         if constexpr (OP == BWD_DX) *at = v;
         else __builtin_nontemporal_store(v, at);
       }
+    }
+  }
+  wave_lds_sync();
+}
+
+// DACT8: the checkpoint's codes and scales for a 32-row block of a wavefront, 8
+// columns per lane, 4 NB lanes per row. All of a block's are fetched before the
+// block before it is stored: a load that follows stores is waited for together
+// with them. (Fetched as each 4 columns are stored: 16384 rows, d = 4096, f =
+// 14336 2257 us instead of 2101; and 2053 with the stores past the caches, the
+// share 190, 184 and 182. The K loop alone takes 1588 and 165.)
+template <int NB>
+struct BlockCodes {
+  uint2 g[2 * NB], u[2 * NB];
+  uint32_t sg[2 * NB], su[2 * NB];
+  // rows past the last re-read it; 32-bit offsets (cap * 2f codes are below 2^32)
+  __device__ __forceinline__ void fetch(const BwdParams& P, const BwdTile& t, int m0, int c0, int lane) {
+    constexpr int L = 4 * NB;
+#pragma unroll
+    for (int j = 0; j < 2 * NB; ++j) {
+      const int r = min(m0 + j * (64 / L) + lane / L, t.rows - 1);
+      const uint32_t at =
+          (uint32_t)(t.row0 + r) * (2 * (uint32_t)P.f) + (uint32_t)(t.col0 + c0 + (lane & (L - 1)) * 8);
+      g[j] = *reinterpret_cast<const uint2*>(P.gu8 + at);
+      u[j] = *reinterpret_cast<const uint2*>(P.gu8 + (at + (uint32_t)P.f));
+      sg[j] = P.gus[at >> 5];
+      su[j] = P.gus[(at + (uint32_t)P.f) >> 5];
+    }
+  }
+};
+
+// store_block of DACT8: 8 columns per lane, whole 128-byte lines (64 with NB = 1).
+template <int NB>
+__device__ __forceinline__ void store_block8(const BwdParams& P, const BwdTile& t, lds_t* wl, const f32x16 (&acc)[NB],
+                                             int m0, int c0, const BlockCodes<NB>& codes, int lane) {
+  constexpr int C = 8 * NB, L = 4 * NB;
+  const int lr = lane & 31, hi = lane >> 5;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *(lds_f32x4*)(wl + lr * (C * 16) + (((b * 8 + 2 * q + hi) ^ (lr & (C - 1))) << 4)) =
+          f32x4{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+  wave_lds_sync();
+  const int c = lane & (L - 1);
+#pragma unroll
+  for (int j = 0; j < 2 * NB; ++j) {
+    const int r = j * (64 / L) + lane / L;
+    const lds_t* at = wl + r * (C * 16);
+    const f32x4 lo = *(const lds_f32x4*)(at + (((2 * c) ^ (r & (C - 1))) << 4));
+    const f32x4 up = *(const lds_f32x4*)(at + (((2 * c + 1) ^ (r & (C - 1))) << 4));
+    float g[8], u[8], a[8], dg[8], du[8];
+    mxint8_values8(codes.g[j], mxint8_step(codes.sg[j]), g);
+    mxint8_values8(codes.u[j], mxint8_step(codes.su[j]), u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) swiglu_grad(i < 4 ? lo[i] : up[i - 4], g[i], u[i], a[i], dg[i], du[i]);
+    if (m0 + r < t.rows) {
+      const size_t row = (size_t)t.row0 + m0 + r;
+      const int col = t.col0 + c0 + c * 8;
+      auto put = [](uint16_t* to, const float(&v)[8]) {
+        const i32x4 w = {(int)pack_bf16(v[0], v[1]), (int)pack_bf16(v[2], v[3]), (int)pack_bf16(v[4], v[5]),
+                         (int)pack_bf16(v[6], v[7])};
+        __builtin_nontemporal_store(w, reinterpret_cast<i32x4*>(to));
+      };
+      uint16_t* dh = P.dH + row * (2 * (size_t)P.f) + col;
+      put(P.act + row * P.f + col, a);
+      put(dh, dg);
+      put(dh + P.f, du);
     }
   }
   wave_lds_sync();
@@ -440,7 +493,19 @@ __device__ __forceinline__ void band_tile_body(const BwdParams& P, const BwdTile
       dst[a] = m < t.rows ? P.row_dst[t.row0 + m] : 0;
     }
   }
-  if (wp * (NB * 32) < t.cols) {
+  if constexpr (OP == BWD_DACT8) {
+    if (wp * (NB * 32) < t.cols) {
+      BlockCodes<NB> codes[2];
+      codes[0].fetch(P, t, WQ * 32, wp * (NB * 32), lane);
+#pragma unroll
+      for (int a = 0; a < NM; ++a) {
+        const int m0 = (WQ + 2 * a) * 32;
+        if (a + 1 < NM) codes[(a + 1) & 1].fetch(P, t, m0 + 64, wp * (NB * 32), lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m0 < t.rows) store_block8<NB>(P, t, lds + w * 8192, acc[a], m0, wp * (NB * 32), codes[a & 1], lane);
+      }
+    }
+  } else if (wp * (NB * 32) < t.cols) {
 #pragma unroll
     for (int a = 0; a < NM; ++a) {
       const int m0 = (WQ + 2 * a) * 32;
