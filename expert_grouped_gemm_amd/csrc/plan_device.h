@@ -37,8 +37,9 @@ __device__ __forceinline__ void plan_body(const int32_t* __restrict__ offsets, i
   bool bad = false;
   if (e < El) {
     const int lo = offsets[e], hi = offsets[e + 1];
-    cnt = hi - lo;
-    bad = cnt < 0 || (e == 0 && lo < 0) || (e == El - 1 && hi > cap);
+    // compared, not subtracted: two offsets far apart differ by more than 32 bits hold
+    bad = hi < lo || (e == 0 && lo < 0) || (e == El - 1 && hi > cap);
+    cnt = bad ? 0 : hi - lo;
     nb = (cnt + kBM - 1) / kBM;
   }
   if (__syncthreads_or(bad)) {
