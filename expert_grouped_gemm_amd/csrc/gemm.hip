@@ -2,6 +2,8 @@
 // shape choice, the planning kernel (row bands, readiness counters, expert
 // waves) and the launch sequence of each schedule. The kernel itself is in
 // gemm_device.h.
+#include <type_traits>
+
 #include "gemm_device.h"
 #include "plan_device.h"
 
@@ -30,7 +32,9 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
 // null. What earlier calls on the workspace reported stays: a timed-out wait,
 // and the bits `keep` of the argument errors. One block: the whole of plan_body
 // plus these checks took 12 us on the share (4096 rows, 32 experts), this takes
-// 5 (16384 rows 16, 65536 rows 46: one workgroup reads every index).
+// 5 (16384 rows 8, 65536 rows 13: one workgroup reads every index, as many at a
+// time as it can: with 4 in flight per thread, of 256 up to a capacity of 65536
+// rows, those were 17 and 45).
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ offsets, int El, int cap,
                                                          const int32_t* __restrict__ row_src, int64_t src_end,
                                                          const int32_t* __restrict__ row_dst, int keep, int mark,
@@ -50,20 +54,26 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
   __syncthreads();
   int bits = hi < lo || first < 0 || last > cap ? ARG_ERR_OFFSETS : 0;
   const int r_end = min(cap, last);
-  for (int r = max(0, first) + e; r < r_end; r += 4 * (int)blockDim.x) {
-    int src[4], dst[4];
+  // N indices of either array per thread, all in flight together
+  auto check = [&](int r0, auto n) {
+    constexpr int N = decltype(n)::value;
+    int src[N], dst[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = min(r + (int)blockDim.x * i, r_end - 1);
+    for (int i = 0; i < N; ++i) {
+      const int q = min(r0 + e + (int)blockDim.x * i, r_end - 1);
       src[i] = row_src ? row_src[q] : 0;
       dst[i] = row_dst ? row_dst[q] : 0;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       if (src[i] < 0 || src[i] >= src_end) bits |= ARG_ERR_ROW_SRC;
       if ((unsigned)dst[i] >= (unsigned)cap) bits |= ARG_ERR_ROW_DST;
     }
-  }
+    return r0 + N * (int)blockDim.x;
+  };
+  for (int r = max(0, first); r < r_end;)
+    r = r_end - r > 4 * (int)blockDim.x ? check(r, std::integral_constant<int, 16>{})
+                                        : check(r, std::integral_constant<int, 4>{});
   if (bits) atomicOr(&err, bits);
   // ranks: the full bands of the experts before this one, and the experts
   // before it (in this wavefront; those of other wavefronts below) with a last
@@ -137,7 +147,7 @@ hipError_t launch_plan_rows(const moe_problem_t& p, const Layout& L, char* ws, c
                             const int32_t* row_src, const int32_t* row_dst, int keep, int mark, hipStream_t s) {
   auto I = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
   // a thread per expert at least; enough of them for the row indices
-  const int threads = L.E_l > 256 || L.cap > 65536 ? 1024 : 256;
+  const int threads = L.E_l > 256 || L.cap > 8192 ? 1024 : 256;
   hipLaunchKernelGGL(plan_rows_kernel, dim3(1), dim3(threads), 0, s, offsets, L.E_l, L.cap, row_src, (int64_t)p.T * p.k,
                      row_dst, keep, mark, I(L.band_expert), I(L.band_row0), I(L.band_rows), I(L.pub.meta));
   return hipGetLastError();
