@@ -27,18 +27,19 @@
 // Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
 // without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
 // but for the weight gradients, whose tiles of two to five stages are half setup
-// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DACT8 205 (from a checkpoint, 5.1
+// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DACT8 182 (from a checkpoint, 5.8
 // with its codes and results), DX 386 (4.9), DW2 255 (3.7), DW1 502 (3.7). 16384 rows
 // of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy 55-59% of the
 // time at the clock the chip holds under them, and the loads and LDS reads that
 // do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the epilogue's 3.3
-// GB), DACT8 2210 (870), DX 3408 (1129), DW2 1680 (1145), DW1 3400 (1132).
+// GB), DACT8 2053 (937), DX 3408 (1129), DW2 1680 (1145), DW1 3400 (1132).
 // No kernel here spills a register.
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
 // fragments read across the barrier (20% slower) and every wavefront loading
 // (6%), both on eight wavefronts and while the loads still went through the
-// builtin (see dma16); DACT's gate and up values all fetched ahead of its stores,
-// in fp32 or as codes (registers spilled).
+// builtin (see dma16); DACT's fp32 gate and up values all fetched ahead of its
+// stores (registers spilled); every second XCD half a tile out of step with the
+// others, so that their epilogues' traffic spreads (DACT8 60 us of 2053).
 #pragma once
 
 #include "gemm_device.h"

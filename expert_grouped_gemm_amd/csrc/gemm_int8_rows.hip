@@ -14,6 +14,11 @@
 // One launch: every workgroup reads the offsets and checks the row indices for
 // itself (a few thousand at most, from the L2), to the same verdict, and the
 // first one leaves the report in the workspace.
+//
+// Bound by HBM and the last-level cache: one token, two experts, d = 4096, f =
+// 14336, Linear-1 46 us for 235 MB, 5.1 TB/s; 64 tokens on 32 of 256 experts, d =
+// 7168, f = 2048, Linear-2 70 us for 411 MB, 5.9. (Against the persistent GEMM:
+// few_rows in gemm.hip.)
 #include "gemm_device.h"
 
 namespace moe {
