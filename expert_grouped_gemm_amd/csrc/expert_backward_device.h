@@ -29,9 +29,9 @@
 // but for the weight gradients, whose tiles of two to five stages are half setup
 // and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DACT8 182 (from a checkpoint, 5.8
 // with its codes and results), DX 386 (4.9), DW2 255 (3.7), DW1 502 (3.7). 16384 rows
-// of 8 experts, d = 4096, f = 14336, bound by the MFMA units, busy 55-59% of the
-// time at the clock the chip holds under them, and the loads and LDS reads that
-// do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the epilogue's 3.3
+// of 8 experts, d = 4096, f = 14336, bound by the power the chip allows the MFMA
+// units (DX: busy 67% at 1.63 GHz, DW1: 56% at 1.93) and the loads, LDS reads and
+// stores that do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the epilogue's 3.3
 // GB), DACT8 2053 (937), DX 3408 (1129), DW2 1680 (1145), DW1 3400 (1132).
 // No kernel here spills a register.
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
