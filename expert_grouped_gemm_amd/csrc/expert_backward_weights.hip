@@ -118,8 +118,9 @@ __device__ __forceinline__ BwdTile short_tile(const BwdParams& P, int e, int m, 
 // flight; from step 1 on, each step refills the slot of the step before it.
 // (One stream of stages over a workgroup's tiles, the next one's first loads
 // issued before the last one's stores, was no faster: share dW1 508 against 502
-// us. MFMAs, LDS and stores, 123, 140 and 345 us of them, are what does not
-// overlap.)
+// us; nor were 128 x 128 tiles with three workgroups per CU, 485 against 462, nor
+// parts of every expert kept on one XCD, 464. MFMAs, LDS and stores, 123, 140 and
+// 345 us of them, are what does not overlap.)
 template <int OP>
 __global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kShortRing * kShortStage];
