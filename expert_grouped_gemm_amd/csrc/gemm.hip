@@ -338,19 +338,32 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
 
 // Whether the kernel for few rows takes a Linear on 8-bit integers: at most 8 rows
 // per expert, if the router spreads them evenly (the host does not see the
-// call's offsets; an expert with more than 32 takes passes of 32). Whole calls of
-// the persistent GEMM / of that kernel, us, Linear-1 and Linear-2:
+// call's offsets; an expert with more than 32 takes passes of 32), or 64 where
+// the persistent GEMM's tiles of one band per expert leave three CUs of four
+// idle. Whole calls of the persistent GEMM / of that kernel, us, Linear-1 and
+// Linear-2:
 //   rows per expert (tokens)     1/4 (1)      1 (4)        4 (16)       16 (64)      32 (128)
 //   8 experts, d 4096, f 14336   60/45 68/34  120/87 70/53 185/141 89/72 188/154 89/78 172/225 97/121
 //                                1/2 (16)     2 (64)       8 (256)      16 (512)
 //   32 of 256, d 7168, f 2048    85/65 52/38  156/125 81/69 146/143 90/80 147/155 94/95
 //                                1/4 (4)      4 (64)       8 (128)      16 (256)
 //   64 of 2048, 1024             24/17 16/11  61/50 40/30  51/50 34/31  51/56 35/37
+// and by the tiles, one Linear each:
+//   rows per expert              16       32       64       128
+//   1 expert, 4224 x 384, 3      24/10    24/11    24/13    28/22
+//   1, 14336 x 4096, 16          62/31    62/38    64/54    77/102
+//   4, 4096 x 1408, 44           26/15    26/17    27/24    30/42
+//   8, 1408 x 2048, 64           16/9     16/10    17/12    19/18
+//   8, 2048 x 1408, 88           19/16    19/19    19/24    21/41
+//   1, 4096 x 14336, 112         32/27    31/30    33/42    35/77
+//   64, 384 x 640, 320           19/21    20/23    22/36    26/61
 // A padded layout (its own row_capacity) is the persistent GEMM's: its rows may be
 // many more than the router's.
-static bool few_rows(const moe_problem_t& p) {
-  return (int64_t)p.T * p.k <= 8 * (int64_t)p.E_global &&
-         row_capacity(p) == (int64_t)p.T * (p.k < p.e_end - p.e_begin ? p.k : p.e_end - p.e_begin);
+static bool few_rows(const moe_problem_t& p, bool first, int G) {
+  const int El = p.e_end - p.e_begin;
+  const int64_t tiles = (int64_t)El * (((first ? 2 * (int64_t)p.f : p.d) + 255) / 256);
+  const int rows = 4 * tiles <= G ? 64 : 8;
+  return (int64_t)p.T * p.k <= rows * (int64_t)p.E_global && row_capacity(p) == (int64_t)p.T * (p.k < El ? p.k : El);
 }
 
 // One Linear of the experts on 8-bit integers (see moe_int8_linear1 /
@@ -371,7 +384,7 @@ hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws,
   P.a_k = p.k;
   P.trace = nullptr;
   P.mode = first ? MODE_SEP_L1 : MODE_SEP_L2;
-  if (few_rows(p)) return launch_int8_rows(P, RowsPlan{offsets, L.E_l, (int64_t)p.T * p.k, keep, mark}, G, s);
+  if (few_rows(p, first, G)) return launch_int8_rows(P, RowsPlan{offsets, L.E_l, (int64_t)p.T * p.k, keep, mark}, G, s);
   const hipError_t e = launch_plan_rows(p, L, ws, offsets, row_src, row_dst, keep, mark, s);
   if (e != hipSuccess) return e;
   return launch_gemm_int8(P, G, s);

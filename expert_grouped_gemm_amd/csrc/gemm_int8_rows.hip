@@ -1,7 +1,7 @@
 // The experts' Linears on 8-bit integers for experts of few rows (decoding
-// steps): the weights' bytes are all that counts, and the persistent GEMM's
-// tiles of 128 or 256 weight rows are too few and too coarse to spread over the
-// CUs.
+// steps) and for little weight: the weights' bytes, or the latency of a long K, are
+// all that counts, and the persistent GEMM's tiles of 128 or 256 weight rows are
+// too few and too coarse to spread over the CUs.
 //
 // A unit is 32 weight rows of one expert (Linear-1: 16 gate rows and the 16 up
 // rows of the same SwiGLU columns) over all of K. Its workgroup's four
@@ -19,6 +19,8 @@
 // 14336, Linear-1 46 us for 235 MB, 5.1 TB/s; 64 tokens on 32 of 256 experts, d =
 // 7168, f = 2048, Linear-2 70 us for 411 MB, 5.9. (Against the persistent GEMM:
 // few_rows in gemm.hip.)
+#include <type_traits>
+
 #include "gemm_device.h"
 
 namespace moe {
@@ -167,10 +169,25 @@ __device__ __forceinline__ bool plan_few_rows(const RowsPlan& R, const GemmParam
     if (hi > lo) bands += (int)(((int64_t)hi - lo + kBM - 1) / kBM);
   }
   const int r_end = min(P.cap, last);
-  for (int r = max(0, first) + tid; r < r_end; r += kRowsWaves * 64) {
-    if (P.a_src && (P.a_src[r] < 0 || P.a_src[r] >= R.src_end)) bits |= ARG_ERR_ROW_SRC;
-    if (P.row_dst && (unsigned)P.row_dst[r] >= (unsigned)P.cap) bits |= ARG_ERR_ROW_DST;
-  }
+  auto check = [&](int r0, auto n) {  // N of either array per thread in flight
+    constexpr int N = decltype(n)::value;
+    int src[N], dst[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = min(r0 + i * kRowsWaves * 64 + tid, r_end - 1);
+      src[i] = P.a_src ? P.a_src[r] : 0;
+      dst[i] = P.row_dst ? P.row_dst[r] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (src[i] < 0 || src[i] >= R.src_end) bits |= ARG_ERR_ROW_SRC;
+      if ((unsigned)dst[i] >= (unsigned)P.cap) bits |= ARG_ERR_ROW_DST;
+    }
+    return r0 + N * kRowsWaves * 64;
+  };
+  for (int r = max(0, first); r < r_end;)
+    r = r_end - r > kRowsWaves * 64 ? check(r, std::integral_constant<int, 8>{})
+                                    : check(r, std::integral_constant<int, 1>{});
   __syncthreads();
   if (bits) __hip_atomic_fetch_or((__attribute__((address_space(3))) int*)err, bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
   __syncthreads();

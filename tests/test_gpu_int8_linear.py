@@ -346,6 +346,40 @@ def test_padded_layout():
         assert np.all(np.abs(H[r].double().cpu().numpy() - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
 
 
+@pytest.mark.parametrize("counts", [[12, 7, 8, 9], [0, 15, 16, 17], [31, 0, 32, 33], [0, 0, 64, 0], [65, 1, 0, 100],
+                                    [63, 64, 65, 64], [0, 256, 0, 0], [129, 95, 31, 1]])
+@pytest.mark.parametrize("d,f", [(128, 256), (640, 128), (1152, 896)])
+def test_both_kernels_give_the_same_bits(counts, d, f):
+    """At most 64 rows per expert in the mean: a whole grid leaves the tiles of these to the kernel for few rows, a grid
+    of 8 workgroups or fewer to the persistent GEMM. Sums of whole numbers are the same in any order."""
+    E, A = 4, sum(counts)
+    g = torch.Generator().manual_seed(A)
+    (x, xs), (w, ws_) = _rand(g, A, d), _rand(g, E, 2 * f, d)
+    (h, hs), (w2, w2s) = _rand(g, A, f), _rand(g, E, d, f)
+    off, src, dst = np.concatenate([[0], np.cumsum(counts)]), torch.randperm(A, generator=g), torch.randperm(A, generator=g)
+    outs = []
+    for grid in (0, 8, 2):
+        p = moe.make_problem(A, d, f, E, 1, sched="auto", grid=grid)
+        ws = moe.alloc_workspace(p).fill_(255)
+        H, C = torch.zeros(A, f, dtype=torch.bfloat16, device="cuda"), torch.zeros(A, d, device="cuda")
+        moe.int8_linear1(p, x.cuda(), xs.cuda(), _i32(src), _i32(off), w.cuda(), ws_.cuda(), H, ws)
+        moe.int8_linear2(p, h.cuda(), hs.cuda(), _i32(off), _i32(dst), w2.cuda(), w2s.cuda(), C, ws)
+        moe.check_workspace(p, ws)
+        outs.append((H, C))
+    for H, C in outs[1:]:
+        assert torch.equal(H, outs[0][0]) and torch.equal(C, outs[0][1])
+    H, C = (t.double().cpu().numpy() for t in outs[0])
+    X, W, Hq, W2 = _Scaled(x, xs), _Scaled(w, ws_), _Scaled(h, hs), _Scaled(w2, w2s)
+    for e in range(E):
+        r = slice(off[e], off[e + 1])
+        gate, u = np.split(X[src[r].numpy()].times(W[e]), 2, axis=1)
+        ref = gate / (1 + np.exp(-gate)) * u
+        tol = 4 * U * (1.1 * np.abs(u * gate) + np.abs(ref)) + 16 * U * (1 + np.abs(gate)) * np.abs(ref)
+        assert np.all(np.abs(H[r] - ref) <= tol + B * (np.abs(ref) + tol) + 1e-30), e
+        ref = Hq[r].times(W2[e])
+        assert np.all(np.abs(C[dst[r].numpy()] - ref) <= 4 * U * np.abs(ref)), e
+
+
 @pytest.mark.parametrize("E", [8, 1024])
 def test_a_problem_of_any_type_and_schedule(E):
     """The Linears take their operands' type from the call: what the problem names for the layer's own, its schedule and
