@@ -336,38 +336,51 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
   return launch_gemm_w4a4(P, G, s);
 }
 
-// Whether the kernel for few rows takes a Linear on 8-bit integers: at most 8 rows
-// per expert, if the router spreads them evenly (the host does not see the
-// call's offsets; an expert with more than 32 takes passes of 32), or 64 where
-// the persistent GEMM's tiles of one band per expert leave three CUs of four
-// idle. Whole calls of the persistent GEMM / of that kernel, us, Linear-1 and
-// Linear-2:
-//   rows per expert (tokens)     1/4 (1)      1 (4)        4 (16)       16 (64)      32 (128)
-//   8 experts, d 4096, f 14336   60/45 68/34  120/87 70/53 185/141 89/72 188/154 89/78 172/225 97/121
-//                                1/2 (16)     2 (64)       8 (256)      16 (512)
-//   32 of 256, d 7168, f 2048    85/65 52/38  156/125 81/69 146/143 90/80 147/155 94/95
-//                                1/4 (4)      4 (64)       8 (128)      16 (256)
-//   64 of 2048, 1024             24/17 16/11  61/50 40/30  51/50 34/31  51/56 35/37
-// and by the tiles, one Linear each:
-//   rows per expert              16       32       64       128
-//   1 expert, 4224 x 384, 3      24/10    24/11    24/13    28/22
-//   1, 14336 x 4096, 16          62/31    62/38    64/54    77/102
-//   4, 4096 x 1408, 44           26/15    26/17    27/24    30/42
-//   8, 1408 x 2048, 64           16/9     16/10    17/12    19/18
-//   8, 2048 x 1408, 88           19/16    19/19    19/24    21/41
-//   1, 4096 x 14336, 112         32/27    31/30    33/42    35/77
-//   64, 384 x 640, 320           19/21    20/23    22/36    26/61
+// Whether the kernel for few rows takes a Linear on 8-bit integers. It takes an
+// expert's rows in passes of 32, one after the other in the workgroup of a unit,
+// and reads the unit's weights again for each. The host does not see the call's
+// offsets, and the router's mean says little about a share that holds the experts
+// it favours; but a dispatch gives no expert more rows than there are tokens. So:
+// at most 64 tokens and 8 rows per expert in the mean, or, where the persistent
+// GEMM's tiles of one band per expert leave three CUs of four idle, 128 and 64.
+// Whole calls of the persistent GEMM / of the kernel for few rows, us, Linear-1 and
+// Linear-2 (even: every choice as likely; favoured: zipf 1.2, the favoured experts
+// local; one: every token's first choice is one local expert):
+//   tokens                          1            4            16           64           128            256
+//   8 of 8, top-2, d 4096, f 14336
+//     even                          64/48 71/37  134/97 77/64 197/145 82/78 197/157 83/80 183/230 86/118 195/340 90/183
+//     favoured                      63/47 70/35  135/94 70/63 163/113 72/70 192/169 83/94 195/242 98/162 210/381 119/273
+//   32 of 256, top-8, 7168, 2048
+//     even                          40/22 20/12  45/41 36/24  90/72 57/41   155/135 83/71 155/140 85/75  146/145 89/82
+//     favoured                      48/40 35/27  78/73 59/42  152/120 79/62 154/178 94/97 157/242 103/131 183/383 129/189
+//   64 of 64, top-8, 2048, 1024
+//     even                          20/13 16/11  37/26 25/17  62/49 39/31   51/52 33/32   51/59 34/37    54/83 39/47
+//     favoured                      20/13 15/10  35/23 24/17  37/29 25/19   43/45 31/31   61/63 43/41    73/90 51/54
+// and where the tiles are few (in brackets, Linear-1 and Linear-2):
+//   tokens                          64           128          256          512          1024          2048
+//   1 of 256, top-8, 7168, 2048 (16, 28)
+//     even                          37/18 18/11  37/18 18/11  37/19 18/11  37/22 19/12  37/32 19/14   38/32 19/15
+//     one                           38/31 19/14  43/57 21/21  54/105 27/35 66/200 28/63 70/391 30/117 71/790 52/224
+//   20 of 160, top-6, 1024, 256 (40, 80)
+//     even                          15/10 12/10  15/10 12/10  15/10 12/10  14/11 12/11  15/14 12/12   16/16 13/15
+//     favoured                      15/13 12/12  15/17 13/14  20/26 16/18  21/46 17/27  23/87 24/46   24/165 28/81
+//   8 of 64, top-2, 384, 256 (16, 16)
+//     even                          12/9 12/10   12/10 12/9   13/10 12/9   12/10 11/10  12/11 11/9    12/13 12/10
+//     one                           12/10 11/10  12/13 11/10  15/20 12/13  15/34 13/20  16/62 14/33   17/118 15/61
+//   1 of 1, 4096, 4096 (32, 16)     28/25 27/21  30/42 30/36
 // A padded layout (its own row_capacity) is the persistent GEMM's: its rows may be
 // many more than the router's.
 static bool few_rows(const moe_problem_t& p, bool first, int G) {
   const int El = p.e_end - p.e_begin;
   const int64_t tiles = (int64_t)El * (((first ? 2 * (int64_t)p.f : p.d) + 255) / 256);
-  const int rows = 4 * tiles <= G ? 64 : 8;
-  return (int64_t)p.T * p.k <= rows * (int64_t)p.E_global && row_capacity(p) == (int64_t)p.T * (p.k < El ? p.k : El);
+  const bool idle = 4 * tiles <= G;
+  return p.T <= (idle ? 128 : 64) && (int64_t)p.T * p.k <= (idle ? 64 : 8) * (int64_t)p.E_global &&
+         row_capacity(p) == (int64_t)p.T * (p.k < El ? p.k : El);
 }
 
 // One Linear of the experts on 8-bit integers (see moe_int8_linear1 /
-// moe_int8_linear2), as a launch of the persistent GEMM.
+// moe_int8_linear2): the kernel for few rows, which plans for itself, or the plan
+// and the persistent GEMM.
 hipError_t launch_int8_linear(const moe_problem_t& p, const Layout& L, char* ws, bool first, const int8_t* A,
                               const float* A_scale, const int32_t* row_src, const int32_t* offsets,
                               const int32_t* row_dst, const int8_t* W, const float* W_scale, void* out,
