@@ -341,7 +341,7 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
 // and reads the unit's weights again for each. The host does not see the call's
 // offsets, and the router's mean says little about a share that holds the experts
 // it favours; but a dispatch gives no expert more rows than there are tokens. So:
-// at most 64 tokens and 8 rows per expert in the mean, or, where the persistent
+// at most 64 tokens and 16 rows per expert in the mean, or, where the persistent
 // GEMM's tiles of one band per expert leave three CUs of four idle, 128 and 64.
 // Whole calls of the persistent GEMM / of the kernel for few rows, us, Linear-1 and
 // Linear-2 (even: every choice as likely; favoured: zipf 1.2, the favoured experts
@@ -356,6 +356,11 @@ hipError_t launch_mxfp4_linear(const moe_problem_t& p, const Layout& L, char* ws
 //   64 of 64, top-8, 2048, 1024
 //     even                          20/13 16/11  37/26 25/17  62/49 39/31   51/52 33/32   51/59 34/37    54/83 39/47
 //     favoured                      20/13 15/10  35/23 24/17  37/29 25/19   43/45 31/31   61/63 43/41    73/90 51/54
+//   64 tokens                       16 in the mean: even, favoured, one         32 in the mean
+//   8 and 4, top-2, 4096, 14336     194/156 84/79  193/169 82/94  189/167 87/99  111/123 73/73  109/107 74/61  109/106 74/64
+//   8, top-2, 2048, 2048            24/19 20/12    24/21 21/15    24/22 21/15
+//   16, top-4, 4096, 1408           60/39 24/24    59/45 24/27    61/42 24/28
+//   32, top-8, 2048, 1024           29/32 20/21    40/35 27/25    29/34 20/24
 // and where the tiles are few (in brackets, Linear-1 and Linear-2):
 //   tokens                          64           128          256          512          1024          2048
 //   1 of 256, top-8, 7168, 2048 (16, 28)
@@ -374,7 +379,7 @@ static bool few_rows(const moe_problem_t& p, bool first, int G) {
   const int El = p.e_end - p.e_begin;
   const int64_t tiles = (int64_t)El * (((first ? 2 * (int64_t)p.f : p.d) + 255) / 256);
   const bool idle = 4 * tiles <= G;
-  return p.T <= (idle ? 128 : 64) && (int64_t)p.T * p.k <= (idle ? 64 : 8) * (int64_t)p.E_global &&
+  return p.T <= (idle ? 128 : 64) && (int64_t)p.T * p.k <= (idle ? 64 : 16) * (int64_t)p.E_global &&
          row_capacity(p) == (int64_t)p.T * (p.k < El ? p.k : El);
 }
 

@@ -78,7 +78,8 @@ def test_an_expert_that_every_token_reaches_goes_to_the_persistent_kernel(shape,
 BOUNDS = [((1, 2, 8, 8, 512, 1408), False, False), ((64, 8, 256, 32, 1152, 2048), False, False),
           ((65, 8, 256, 32, 2176, 2048), True, True), ((128, 8, 256, 1, 2304, 1408), False, False),
           ((129, 8, 256, 1, 2304, 1408), True, True), ((128, 1, 1, 1, 640, 512), True, True),
-          ((64, 1, 1, 1, 640, 512), False, False)]
+          ((64, 1, 1, 1, 640, 512), False, False), ((64, 2, 8, 8, 2304, 2176), False, False),  # 16 rows in the mean
+          ((64, 2, 4, 4, 4224, 2176), True, True)]  # 32
 
 
 @pytest.mark.parametrize("shape,one,two", BOUNDS)
