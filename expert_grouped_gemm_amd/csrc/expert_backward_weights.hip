@@ -13,16 +13,31 @@
 namespace moe {
 namespace {
 
-// Rows per expert up to which the kernel for few rows runs. Whole calls of
-// moe_expert_backward with it / with the other one and its copies, us:
-//   rows per expert              128          192          256          512          1024
-//   32 experts, d 7168, f 2048   1689 / 1783  2222 / 2209  3040 / 2941  5072 / 4783  8987 / 8234
-//   8 of 4096, 14336             1751 / 1785  2263 / 2229  3312 / 3209  5203 / 4816  9119 / 8108
-//   16 of 2048, 1024              172 / 189    208 / 222    278 / 293    430 / 442    732 / 718
-// They cross between 192 and 640 rows. The rows are the router's mean, T k /
-// E_global, as the host does not see the call's offsets: a share that holds the
-// favoured experts may take the kernel for few rows for long ones.
-constexpr int kShortRows = 256;
+// Rows per expert up to which the kernel for few rows runs: the router's mean, T k /
+// E_global, as the host does not see the call's offsets (a share that holds the
+// favoured experts may take the kernel for few rows for long ones). The other
+// kernel's gain grows with rows x d x f, its copies cost rows x d and a launch: where
+// f is narrow, or all the experts' weights are few, it pays from more rows on. Whole
+// calls of moe_expert_backward with the kernel for few rows / with the other one and
+// its copies, us:
+//   rows per expert              264          384          512
+//   1 expert, d 512, f 512         64 / 72      69 / 77      79 / 85
+//   8 of 2048, 1024               170 / 178    175 / 186    191 / 199
+//   8 of 4096, 1024               305 / 318    323 / 331    354 / 353
+//   1 of 4096, 4096               199 / 205    210 / 216    226 / 229
+//   32 of 1024, 512               184 / 195    194 / 222    219 / 239
+//   64 of 4096, 512              1128 / 1166  1278 / 1313  1383 / 1409
+//   256 of 1024, 512             1252 / 1265  1494 / 1501  1627 / 1630
+// and with 3 2^24 elements of W2 or more and a wider f:
+//   24 of 2048, 1024              433 / 446    492 / 492    582 / 568
+//   12 of 2048, 2048              457 / 455    511 / 498    616 / 589
+//   3 of 4096, 4096               435 / 431    491 / 484    601 / 578
+//   64 of 4096, 768              1600 / 1576  1859 / 1820  2038 / 1975
+//   32 of 7168, 2048             3603 / 3426 (300 rows)    4449 / 4132
+//   8 of 4096, 14336             3649 / 3411 (300 rows)    4398 / 3967
+// (128 and 192 rows of the last two: 1689 / 1783 and 2222 / 2209, 1751 / 1785 and
+// 2263 / 2229.)
+constexpr int kShortRows = 256, kShortRowsOfLittle = 512;
 
 // ------------------------------------------------------------- few rows
 
@@ -454,7 +469,8 @@ __global__ __launch_bounds__(kLongThreads, 1) void expert_backward_kernel<BWD_DW
 }  // namespace
 
 bool long_experts(const moe_problem_t& p) {
-  return (int64_t)p.T * p.k > (int64_t)kShortRows * p.E_global;
+  const bool little = p.f <= 512 || (int64_t)(p.e_end - p.e_begin) * p.d * p.f < 3 << 24;
+  return (int64_t)p.T * p.k > (int64_t)(little ? kShortRowsOfLittle : kShortRows) * p.E_global;
 }
 
 hipError_t launch_weight_gradients(const BwdParams& P, bool long_rows, int G, hipStream_t s) {
