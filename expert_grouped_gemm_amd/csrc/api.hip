@@ -88,7 +88,8 @@ bool shares_bytes(std::initializer_list<Span> outputs, std::initializer_list<Spa
 Span workspace_tables(const moe::Layout& L, const void* ws) { return {ws, L.pub.topk_idx}; }
 
 // The experts' gradient addresses the 256 rows of a tile by 32-bit offsets (of
-// rows up to 4 f bytes).
+// rows up to 4 f bytes); the forward pass that leaves its checkpoint takes no wider
+// ones (its tiles' 128 weight rows of either half would pass 32 bits beyond 2^24).
 bool backward_widths_ok(const moe_problem_t& p) { return p.d <= 1 << 20 && p.f <= 1 << 20; }
 
 // The 8-bit integer sums of K products of codes in [-128, 127] fit 32 bits.
@@ -674,7 +675,7 @@ MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const
                                                    void* workspace, size_t ws_bytes, void* stream) {
   moe_status_t st = check_problem(p);
   if (st != MOE_OK) return st;
-  if (p->dtype != MOE_DTYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (p->dtype != MOE_DTYPE_BF16 || !backward_widths_ok(*p)) return MOE_ERR_UNSUPPORTED;
   if (!X || !offsets || !row_dst || !W1 || !W2 || !gu || !gu_scale || !combine_buf) return MOE_ERR_INVALID_ARGUMENT;
   for (const void* q : {X, W1, W2, (const void*)gu, (const void*)gu_scale, (const void*)combine_buf})
     if (!aligned16(q)) return MOE_ERR_INVALID_ARGUMENT;

@@ -620,7 +620,7 @@ MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* s
  * the forward pass leaves the SwiGLU inputs in MXINT8, 2f (1 + 1/32) bytes a
  * row, and the backward pass takes them from there instead of multiplying the
  * tokens with W1 again (a quarter of moe_expert_backward's operations). bf16
- * only (MOE_ERR_UNSUPPORTED otherwise).
+ * only, d and f at most 2^20 (MOE_ERR_UNSUPPORTED otherwise).
  *
  * moe_expert_forward_checkpoint: moe_expert_forward (bf16; its combine_buf, bit
  * for bit, in the separate schedule) on the tokens X bf16 [T, d] through row_src
@@ -635,8 +635,7 @@ MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* s
  * moe_expert_backward_checkpoint: moe_expert_backward with the gate and up
  * values read from gu and gu_scale. X is bf16 as there (X_scale NULL), or int8
  * MXINT8 codes of the same shape with X_scale uint8 [rows, d/32]. Its roundings
- * and checks are moe_expert_backward's, d and f at most 2^20; every array
- * 16-byte aligned. workspace: moe_checkpoint_workspace_size(p) bytes (0 for an
+ * and checks are moe_expert_backward's; every array 16-byte aligned. workspace: moe_checkpoint_workspace_size(p) bytes (0 for an
  * invalid or non-bf16 problem), which serves the forward calls too. */
 MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const void* X, const int32_t* row_src,
                                                    const int32_t* offsets, const int32_t* row_dst, const void* W1,
