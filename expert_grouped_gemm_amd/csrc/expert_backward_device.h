@@ -14,7 +14,9 @@
 //   DW2   dW2[e] = do^T a    both strided along K = the expert's rows
 //   DW1   dW1[e] = dh^T x    both strided along K
 // a and dh are rounded to bf16, the operand type of the products they enter
-// (a as in the forward); every sum is fp32, dx and the weight gradients are
+// (a as in the forward; the outputs are then off by 2.34e-3 of their norm, where
+// rounding the exact ones costs 1.66e-3, and two bf16 terms instead of one would
+// double three products); every sum is fp32, dx and the weight gradients are
 // rounded once. Every output element is one workgroup's sum in one K order:
 // no atomics, the same result on every call.
 //
@@ -24,15 +26,17 @@
 // (ds_read_b64_tr_b16: 16 lanes take 4 K rows x 16 columns, lane i ends with
 // the 4 K values of column i), so no operand is ever transposed in memory.
 //
-// Measured (us; rates in TFLOP/s or TB/s of the bytes the product cannot do
-// without). The share (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM
-// but for the weight gradients, whose tiles of two to five stages are half setup
-// and stores: GU 356 (5.3 TB/s), DACT 183 (5.1), DACT8 182 (from a checkpoint, 5.8
-// with its codes and results), DX 386 (4.9), DW2 255 (3.7), DW1 502 (3.7). 16384 rows
-// of 8 experts, d = 4096, f = 14336, bound by the power the chip allows the MFMA
-// units (DX: busy 67% at 1.63 GHz, DW1: 56% at 1.93) and the loads, LDS reads and
-// stores that do not overlap with them: GU 3564 (1080), DACT 2282 (843, with the epilogue's 3.3
-// GB), DACT8 2053 (937), DX 3408 (1129), DW2 1680 (1145), DW1 3400 (1132).
+// Measured (medians of whole calls' launches over three sets of operands in turn, us;
+// rates in TFLOP/s or TB/s of the bytes the product cannot do without). The share
+// (4096 rows of 32 experts, d = 7168, f = 2048), bound by HBM but for the weight
+// gradients, whose tiles of two to five stages are half setup and stores: GU 364 (5.2
+// TB/s), DACT 195 (4.8), DACT8 200 (from a checkpoint, 5.3 with its codes and
+// results), DX 386 (4.9), DW2 320-340 (2.8), DW1 586 (3.2; 484 where the tokens' codes
+// have been expanded into expert order). 16384 rows of 8 experts, d = 4096, f = 14336:
+// the MFMA units at the clock that their power leaves (DX: busy 67% at 1.63 GHz, DW1:
+// 56% at 1.93), and the loads, LDS reads, epilogues and last rounds that do not
+// overlap with them: GU 3606 (1067), DACT 2338 (823, with the epilogue's 3.3 GB),
+// DACT8 2060 (934), DX 3410-3460 (1120), DW2 1870 (1029), DW1 3530 (1090).
 // No kernel here spills a register.
 // Not kept: a ring of 32-wide K stages with the loads spread over the MFMAs and
 // fragments read across the barrier (20% slower) and every wavefront loading
@@ -335,7 +339,7 @@ __device__ __forceinline__ void store_block(const BwdParams& P, const BwdTile& t
 // block before it is stored: a load that follows stores is waited for together
 // with them. (Fetched as each 4 columns are stored: 16384 rows, d = 4096, f =
 // 14336 2257 us instead of 2101; and 2053 with the stores past the caches, the
-// share 190, 184 and 182. The K loop alone takes 1588 and 165.)
+// share 190, 184 and 182, each timed by itself. The K loop alone takes 1588 and 165.)
 template <int NB>
 struct BlockCodes {
   uint2 g[2 * NB], u[2 * NB];

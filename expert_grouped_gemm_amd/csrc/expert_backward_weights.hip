@@ -135,7 +135,8 @@ __device__ __forceinline__ BwdTile short_tile(const BwdParams& P, int e, int m, 
 // issued before the last one's stores, was no faster: share dW1 508 against 502
 // us; nor were 128 x 128 tiles with three workgroups per CU, 485 against 462, nor
 // parts of every expert kept on one XCD, 464. MFMAs, LDS and stores, 123, 140 and
-// 345 us of them, are what does not overlap.)
+// 345 us of them, are what does not overlap. All timed by themselves; in whole calls
+// the share's dW1 takes 484 to 586.)
 template <int OP>
 __global__ __launch_bounds__(256, 2) void weight_backward_short_kernel(BwdParams P) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kShortRing * kShortStage];
@@ -302,11 +303,11 @@ __device__ __forceinline__ void long_store(const BwdParams& P, const LongTile& t
 // order that the compiler is held to; with one wavefront per SIMD nothing else
 // fills a gap. Nothing in the loop depends on the stream's end: behind the last
 // tile its last stage is loaded again, into slots that nothing reads.
-// 16384 rows of 8 experts, d = 4096, f = 14336, us (TFLOP/s): DW2 1680 (1145), DW1
-// 3400 (1132), the MFMAs busy 55% of the time at the 1.96 GHz the chip holds; the
-// loop's bookkeeping as it stands, instead of counts of what each wait may leave
-// in flight, and the order of its reads took them from 2220 and 4370. (256 x 256
-// tiles on eight wavefronts, 128 x 64 each, two stages of 64: 1750 and 3660.)
+// 16384 rows of 8 experts, d = 4096, f = 14336, in whole calls, us (TFLOP/s): DW2 1870
+// (1029), DW1 3530 (1090), the MFMAs busy 55% of the time at the 1.96 GHz the chip
+// holds. (256 x 256 tiles on eight wavefronts, 128 x 64 each, two stages of 64: 1875
+// and 3730; whole calls of 512 rows per expert 4398 instead of 3967. Counts of what
+// each wait may leave in flight, and the reads in another order: 2220 and 4370.)
 template <int OP>
 __device__ __forceinline__ void weight_tiles_long(const BwdParams& P, lds_t* lds) {
   const int G = gridDim.x;

@@ -80,8 +80,10 @@ __device__ __forceinline__ float row_scale(float amax) {
 
 // A row per LPR lanes, its values in registers between the maximum and the
 // codes (CH groups of 8 per lane; a row with more is read again), so that a row
-// is read once. Bound by HBM: 16384 x 14336 bf16 values 131 us for 705 MB, 5.4
-// TB/s. The fewest lanes of 16, 64, 256 and 512 whose registers hold the row
+// is read once. Bound by HBM: 16384 x 14336 bf16 values 138 us for 705 MB, 5.1
+// TB/s, over three sets of arrays in turn (160 between calls of the inverse, whose
+// 940 MB of results are still on their way), fp32 ones 212 us for 1175 MB, 5.5 (243).
+// The fewest lanes of 16, 64, 256 and 512 whose registers hold the row
 // (bf16, us, with 16 / 64 / 256 / 512 lanes): 65536 x 128 7.7 / 22 / 63 / 136,
 // x 512 19 / 24 / 66 / 142, x 2048 - / 77 / 96 / 177, 32768 x 7168 - / - / 130 /
 // 147, 16384 x 14336 - / - / 134 / 131 (1024 lanes 192).
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(LPR > 256 ? LPR : 256) void int8_quantize_kernel(co
 
 // code * scale: four values per lane. A lane's group and row advance by the
 // grid's step, drow rows and dcol groups of gpr to a row. Bound by HBM: 16384 x
-// 14336 to fp32 207 us for 1175 MB, 5.7 TB/s.
+// 14336 to fp32 212 us for 1175 MB, 5.5 TB/s, to bf16 146 for 705, 4.8.
 template <bool F32_OUT>
 __global__ __launch_bounds__(256) void int8_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                               const float* __restrict__ scales, int64_t n4,
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(256) void int8_dequantize_kernel(const uint32_t* __
 // of two, so the quotient is exact and so is every value read back, in bf16
 // too (7 bits of magnitude). Four consecutive lanes hold a block, 8 elements
 // each. Bound by HBM: 32768 x 7168 bf16 values 138 us for 712 MB, 5.2 TB/s, and
-// back 115 us, 6.2.
+// back 115 us, 6.2; fp32 ones 217 us for 1182 MB, 5.4, and back 296, 4.0.
 template <bool F32_IN>
 __global__ __launch_bounds__(256) void mxint8_quantize_kernel(const void* __restrict__ x, int64_t n8,
                                                               uint2* __restrict__ codes,

@@ -569,6 +569,9 @@ MOE_API moe_status_t moe_int8_dequantize(const int8_t* codes, const float* scale
  * MXFP4 Linears. A layer forward is
  *   moe_int8_quantize(X) -> moe_int8_linear1 -> moe_int8_quantize(H)
  *   -> moe_int8_linear2 -> moe_combine.
+ * The row count of a quantiser is the host's: where only offsets[E_l] on the
+ * device holds H's, quantise the capacity (what is behind the last row is not
+ * used).
  *
  * moe_int8_linear1: X int8 [T, d], X_scale fp32 [T] with row_src int32 [cap]
  * (row r reads token row_src[r] / k), or, with row_src NULL, X int8 [cap, d]
@@ -627,7 +630,10 @@ MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* s
  * int32 [cap], or with row_src NULL on rows in expert order [cap, d].
  *   gu int8 [cap, 2f], gu_scale uint8 [cap, 2f/32] out: the fp32 products
  *   W1[e] x of row r, gate [0, f) and up [f, 2f), as moe_mxint8_quantize leaves
- *   them. Rows past the last stay as they were.
+ *   them. Rows past the last stay as they were. Both hold the row capacity, T *
+ *   min(k, E_l) rows or p->row_capacity, of which a share uses offsets[E_l]: a
+ *   caller that keeps checkpoints of many layers can copy those rows away and
+ *   back, nothing behind them is read.
  * workspace: moe_workspace_size(p). Device-side checks as in
  * moe_mxfp4_linear1 (offsets, row_src, row_dst): if one fails no output is
  * written.
@@ -636,7 +642,8 @@ MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* s
  * values read from gu and gu_scale. X is bf16 as there (X_scale NULL), or int8
  * MXINT8 codes of the same shape with X_scale uint8 [rows, d/32]. Its roundings
  * and checks are moe_expert_backward's; every array 16-byte aligned. workspace: moe_checkpoint_workspace_size(p) bytes (0 for an
- * invalid or non-bf16 problem), which serves the forward calls too. */
+ * invalid or non-bf16 problem), which serves the forward calls too; it has room
+ * for the rows of MXINT8 tokens as bf16, whichever X a call brings. */
 MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const void* X, const int32_t* row_src,
                                                    const int32_t* offsets, const int32_t* row_dst, const void* W1,
                                                    const void* W2, int8_t* gu, uint8_t* gu_scale, void* combine_buf,
