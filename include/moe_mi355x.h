@@ -641,9 +641,10 @@ MOE_API moe_status_t moe_mxint8_dequantize(const int8_t* codes, const uint8_t* s
  * moe_expert_backward_checkpoint: moe_expert_backward with the gate and up
  * values read from gu and gu_scale. X is bf16 as there (X_scale NULL), or int8
  * MXINT8 codes of the same shape with X_scale uint8 [rows, d/32]. Its roundings
- * and checks are moe_expert_backward's; every array 16-byte aligned. workspace: moe_checkpoint_workspace_size(p) bytes (0 for an
- * invalid or non-bf16 problem), which serves the forward calls too; it has room
- * for the rows of MXINT8 tokens as bf16, whichever X a call brings. */
+ * and checks are moe_expert_backward's; every array 16-byte aligned. workspace:
+ * moe_checkpoint_workspace_size(p) bytes (0 for an invalid or non-bf16 problem, or
+ * wider rows), which serves the forward calls too; it has room for the rows of
+ * MXINT8 tokens as bf16, whichever X a call brings. */
 MOE_API moe_status_t moe_expert_forward_checkpoint(const moe_problem_t* p, const void* X, const int32_t* row_src,
                                                    const int32_t* offsets, const int32_t* row_dst, const void* W1,
                                                    const void* W2, int8_t* gu, uint8_t* gu_scale, void* combine_buf,
